@@ -24,6 +24,7 @@ from ._native import (  # noqa: F401
     EventOverlap,
     Handle,
     LibraryMissing,
+    RouteConfig,
     STATUS_ROUTING,
     STATUS_TRUNCATED,
     Status,
@@ -35,8 +36,13 @@ from ._native import (  # noqa: F401
     debug_e4m3_encode,
     dispatch,
     dispatch_cached,
+    expert_rows,
     get_layout,
     lib,
     lib_path,
+    matmul_int8,
+    quantize_int8,
     relayout,
+    route,
+    route_backward,
 )

@@ -9,7 +9,7 @@ import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libep_mi355x.so"
-EP_ABI_VERSION = 4
+EP_ABI_VERSION = 5
 
 # dispatch flags
 _FP8 = 1
@@ -17,6 +17,10 @@ _ZERO_PADDING = 2
 _SCALES_COL_MAJOR = 4
 _SCALES_UE8M0 = 8
 _SYMMETRIC_WINDOWS = 1
+# ep_route_config enumerations and ep_matmul_int8 flags
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+_GATED = 1
 # ep_handle_status bits
 STATUS_ROUTING = 1
 STATUS_TRUNCATED = 2
@@ -85,6 +89,19 @@ class _SizeHint(ctypes.Structure):
         "recv_src_meta_bytes", "combine_out_bytes", "total_bytes")]
 
 
+class _RouteConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("num_topk", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 @dataclasses.dataclass(frozen=True)
 class Config:
     """P virtual ranks x S tokens, hidden H, top-K of E experts, expert_alignment A.
@@ -107,6 +124,33 @@ class Config:
     @property
     def T(self) -> int:
         return self.P * self.S
+
+
+@dataclasses.dataclass(frozen=True)
+class RouteConfig:
+    """A router: top-K of E experts by softmax or sigmoid scores.
+
+    num_groups, topk_groups: experts in num_groups groups of consecutive ids, of which a token
+    keeps topk_groups by group_score ("max": a group's largest key, "top2": the sum of its two
+    largest).  renormalize: divide a token's weights by their sum.  scale multiplies them."""
+
+    E: int
+    K: int
+    score: str = "softmax"
+    num_groups: int = 1
+    topk_groups: int = 1
+    group_score: str = "max"
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}, got {self.score!r}")
+        if self.group_score not in _GROUP_SCORES:
+            raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {self.group_score!r}")
+        c = _RouteConfig(self.E, self.K, self.num_groups, self.topk_groups, _SCORES[self.score],
+                         _GROUP_SCORES[self.group_score], int(bool(self.renormalize)), self.scale)
+        object.__setattr__(self, "_struct", c)  # built once: a router is called for every step
 
 
 _lib = None
@@ -148,6 +192,13 @@ def lib() -> ctypes.CDLL:
                    "ep_dispatch_prequant_cached", "ep_combine",
                    "ep_handle_config", "ep_handle_check", "ep_handle_counts", "ep_handle_status",
                    "ep_handle_tensor"):
+            getattr(L, fn).restype = i32
+        L.ep_route.argtypes = [ctypes.POINTER(_RouteConfig), i32, vp, i64, i64, vp, vp, vp, vp, vp]
+        L.ep_route_backward.argtypes = [ctypes.POINTER(_RouteConfig), i32, vp, i64, i64, vp, vp, vp, vp]
+        L.ep_quantize_int8.argtypes = [i32, vp, i64, i32, i64, vp, vp, vp]
+        L.ep_expert_rows.argtypes = [vp, vp, vp, vp]
+        L.ep_matmul_int8.argtypes = [vp, vp, i64, vp, vp, i32, vp, vp, i32, i32, u32, i32, vp, vp]
+        for fn in ("ep_route", "ep_route_backward", "ep_quantize_int8", "ep_expert_rows", "ep_matmul_int8"):
             getattr(L, fn).restype = i32
         L.ep_debug_e4m3_encode.argtypes = [vp, vp, i64, vp]
         L.ep_debug_e4m3_encode.restype = i32
@@ -553,6 +604,170 @@ def combine(h: Handle, y, topk_weights=None, bias=None, out=None, async_with_com
     if not async_with_compute_stream:
         return launch()
     return _overlapped(h, y.device, [y, topk_weights, bias, out], launch, previous_event)
+
+
+_types: dict = {}
+
+
+def _type(t, name):
+    """EP_TYPE_* of a tensor's dtype."""
+    import torch
+
+    if not _types:
+        _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    if t not in _types:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t}")
+    return _types[t]
+
+
+def _require_rows(t, name, cols=None):
+    """A floating device matrix whose rows may be apart; returns (EP_TYPE_*, row stride)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    code = _type(t.dtype, name)
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must have shape [rows, {'columns' if cols is None else cols}], got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return code, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def route(rc: RouteConfig, logits, bias=None, token_mask=None, out=None):
+    """ep_route: router logits [T, E] (float32, bfloat16 or float16, rows may be apart) ->
+    (topk_idx int64 [T, K], topk_weights float32 [T, K]), as get_layout, dispatch and combine
+    take them.
+
+    bias: float32 [E], added to the scores for the choice only; token_mask: bool [T], False
+    leaves a token unrouted (ids -1, weights 0); out: optional (topk_idx, topk_weights)."""
+    import torch
+
+    code, stride = _require_rows(logits, "logits", rc.E)
+    T, device = logits.shape[0], logits.device
+    if bias is not None:
+        _require(bias, torch.float32, (rc.E,), "bias", device)
+    if token_mask is not None:
+        _require(token_mask, torch.bool, (T,), "token_mask", device)
+    if out is None:
+        idx = torch.empty((T, rc.K), dtype=torch.int64, device=device)
+        w = torch.empty((T, rc.K), dtype=torch.float32, device=device)
+    else:
+        idx, w = out
+        _require(idx, torch.int64, (T, rc.K), "topk_idx", device)
+        _require(w, torch.float32, (T, rc.K), "topk_weights", device)
+    with _on(device):
+        _check(lib().ep_route(ctypes.byref(rc._struct), code, _ptr(logits), T, stride, _ptr(bias), _ptr(token_mask),
+                              _ptr(idx), _ptr(w), _stream(device)))
+    return idx, w
+
+
+def route_backward(rc: RouteConfig, logits, topk_idx, grad_weights, out=None):
+    """ep_route_backward: gradient of topk_weights (float32 [T, K]) -> gradient of the logits,
+    [T, E] contiguous in the logits' dtype (out: optional, that tensor)."""
+    import torch
+
+    code, stride = _require_rows(logits, "logits", rc.E)
+    T, device = logits.shape[0], logits.device
+    _require(topk_idx, torch.int64, (T, rc.K), "topk_idx", device)
+    _require(grad_weights, torch.float32, (T, rc.K), "grad_weights", device)
+    if out is None:
+        out = torch.empty((T, rc.E), dtype=logits.dtype, device=device)
+    else:
+        _require(out, logits.dtype, (T, rc.E), "grad_logits", device)
+    with _on(device):
+        _check(lib().ep_route_backward(ctypes.byref(rc._struct), code, _ptr(logits), T, stride, _ptr(topk_idx),
+                                       _ptr(grad_weights), _ptr(out), _stream(device)))
+    return out
+
+
+def quantize_int8(x, out=None):
+    """ep_quantize_int8: x [N, H] (float32, bfloat16 or float16, rows may be apart) ->
+    (codes int8 [N, H], scales float32 [N]); a weight tensor [outer, inner] gives its codes and
+    per-channel scales.  out: optional (codes, scales)."""
+    import torch
+
+    code, stride = _require_rows(x, "x")
+    N, H = x.shape
+    if out is None:
+        codes = torch.empty((N, H), dtype=torch.int8, device=x.device)
+        scales = torch.empty((N,), dtype=torch.float32, device=x.device)
+    else:
+        codes, scales = out
+        _require(codes, torch.int8, (N, H), "codes", x.device)
+        _require(scales, torch.float32, (N,), "scales", x.device)
+    with _on(x.device):
+        _check(lib().ep_quantize_int8(code, _ptr(x), N, H, stride, _ptr(codes), _ptr(scales), _stream(x.device)))
+    return codes, scales
+
+
+def expert_rows(h: Handle, out=None):
+    """ep_expert_rows -> (row_start int64 [E], row_count int32 [E]) on the device: each expert's
+    rows in the handle's expanded tensors, without padding; nothing is read back."""
+    import torch
+
+    E = h.cfg.E
+    if out is None:
+        start = torch.empty((E,), dtype=torch.int64, device=h.device)
+        count = torch.empty((E,), dtype=torch.int32, device=h.device)
+    else:
+        start, count = out
+        _require(start, torch.int64, (E,), "row_start", h.device)
+        _require(count, torch.int32, (E,), "row_count", h.device)
+    with _on(h.device):
+        _check(lib().ep_expert_rows(h.ptr, _ptr(start), _ptr(count), _stream(h.device)))
+    return start, count
+
+
+def matmul_int8(a, w, rows=None, gated: bool = False, out_dtype=None, out=None):
+    """ep_matmul_int8: a = (codes int8 [M, inner], scales float32 [M]) times
+    w = (codes int8 [outer, inner], scales float32 [outer]), or, with
+    rows = (row_start int64 [G], row_count int32 [G]) as expert_rows gives them,
+    w = (codes int8 [G, outer, inner], scales float32 [G, outer]) -> [M, outer].
+
+    gated: silu(first half of the channels) * second half -> [M, outer / 2].  out_dtype:
+    bfloat16 (default), float16 or float32.  Rows of no group are left as they were in ``out``
+    (without ``out`` they are not initialised)."""
+    import torch
+
+    if not (isinstance(a, tuple) and len(a) == 2 and isinstance(w, tuple) and len(w) == 2):
+        raise TypeError("a and w must be pairs (codes, scales)")
+    (x, xs), (wc, wsc) = a, w
+    for t, name, dims in ((x, "a codes", 2), (wc, "w codes", 3 if rows is not None else 2)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    M, K = x.shape
+    device = x.device
+    _require(x, torch.int8, (M, K), "a codes")
+    _require(xs, torch.float32, (M,), "a scales", device)
+    N = wc.shape[-2]
+    G = wc.shape[0] if rows is not None else 0
+    start = count = None
+    if rows is not None:
+        if G == 0:
+            raise ValueError("w holds no group")
+        start, count = rows
+        _require(start, torch.int64, (G,), "row_start", device)
+        _require(count, torch.int32, (G,), "row_count", device)
+    shape = (G, N, K) if rows is not None else (N, K)
+    _require(wc, torch.int8, shape, "w codes", device)
+    _require(wsc, torch.float32, shape[:-1], "w scales", device)
+    if gated and N % 2:
+        raise ValueError(f"a gated product needs an even number of channels, got {N}")
+    width = N // 2 if gated else N
+    if out is None:
+        out = torch.empty((M, width), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=device)
+    else:
+        _require(out, out.dtype if out_dtype is None else out_dtype, (M, width), "out", device)
+    code = _type(out.dtype, "out")
+    with _on(device):
+        _check(lib().ep_matmul_int8(_ptr(x), _ptr(xs), M, _ptr(wc), _ptr(wsc), G, _ptr(start), _ptr(count), K, N,
+                                    _GATED if gated else 0, code, _ptr(out), _stream(device)))
+    return out
 
 
 def debug_e4m3_encode(q):

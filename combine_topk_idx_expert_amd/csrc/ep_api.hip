@@ -17,7 +17,9 @@
 
 #include "ep_mi355x.h"
 #include "ep_dispatch.hpp"
+#include "ep_int8.hpp"
 #include "ep_layout.hpp"
+#include "ep_route.hpp"
 
 using namespace ep;
 
@@ -427,6 +429,7 @@ ep_status check_device(const ep_handle* h) {
 }
 
 #include "ep_launch.hpp"
+#include "ep_ops_launch.hpp"
 
 }  // namespace
 
@@ -690,6 +693,99 @@ ep_status ep_combine(const ep_handle* h, const void* y, const float* topk_weight
   CombineArgs a{(const uint16_t*)y, topk_weights, h->dst_row, (const uint16_t*)bias, (uint16_t*)out,
                 (int)h->T, h->dims.K, h->cfg.hidden, 1};
   return launch_combine(a, (hipStream_t)stream);
+}
+
+ep_status ep_route(const ep_route_config* cfg, int32_t type, const void* logits, int64_t num_tokens,
+                   int64_t row_stride, const float* bias, const uint8_t* token_mask, int64_t* topk_idx,
+                   float* topk_weights, void* stream) {
+  ep_status st = validate_route(cfg, type, num_tokens, row_stride);
+  if (st != EP_OK) return st;
+  if (num_tokens == 0) return EP_OK;
+  if (!logits || !topk_idx || !topk_weights) return fail(EP_ERR_NULL, "logits / topk_idx / topk_weights is NULL");
+  if (misaligned(logits, type_bytes(type)) || misaligned(bias, 4) || misaligned(topk_idx, 8) ||
+      misaligned(topk_weights, 4))
+    return fail(EP_ERR_SHAPE, "logits / bias / topk_idx / topk_weights must be aligned to their element size");
+  RouteArgs a{logits, row_stride, bias, token_mask, topk_idx, topk_weights, (int)num_tokens, cfg->num_experts,
+              cfg->num_topk, cfg->num_groups, cfg->topk_groups, cfg->score == EP_SCORE_SIGMOID,
+              cfg->group_score == EP_GROUP_TOP2, cfg->renormalize != 0, cfg->scale};
+  return with_type(type, [&](auto io) { return launch_route<decltype(io)>(a, (hipStream_t)stream); });
+}
+
+ep_status ep_route_backward(const ep_route_config* cfg, int32_t type, const void* logits, int64_t num_tokens,
+                            int64_t row_stride, const int64_t* topk_idx, const float* grad_weights,
+                            void* grad_logits, void* stream) {
+  ep_status st = validate_route(cfg, type, num_tokens, row_stride);
+  if (st != EP_OK) return st;
+  if (num_tokens == 0) return EP_OK;
+  if (!logits || !topk_idx || !grad_weights || !grad_logits)
+    return fail(EP_ERR_NULL, "logits / topk_idx / grad_weights / grad_logits is NULL");
+  if (misaligned(logits, type_bytes(type)) || misaligned(grad_logits, type_bytes(type)) || misaligned(topk_idx, 8) ||
+      misaligned(grad_weights, 4))
+    return fail(EP_ERR_SHAPE, "logits / topk_idx / grad_weights / grad_logits must be aligned to their element size");
+  RouteBwdArgs a{logits, row_stride, topk_idx, grad_weights, grad_logits, (int)num_tokens, cfg->num_experts,
+                 cfg->num_topk, cfg->score == EP_SCORE_SIGMOID, cfg->renormalize != 0, cfg->scale};
+  return with_type(type, [&](auto io) { return launch_route_backward<decltype(io)>(a, (hipStream_t)stream); });
+}
+
+ep_status ep_quantize_int8(int32_t type, const void* x, int64_t num_rows, int32_t num_cols, int64_t row_stride,
+                           int8_t* codes, float* scales, void* stream) {
+  if (type != EP_TYPE_F32 && type != EP_TYPE_BF16 && type != EP_TYPE_F16)
+    return fail(EP_ERR_SHAPE, "unknown element type %d", type);
+  if (num_rows < 0 || num_cols < 1) return fail(EP_ERR_SHAPE, "bad sizes: %lld rows of %d", (long long)num_rows, num_cols);
+  if (num_rows == 0) return EP_OK;
+  if (row_stride < num_cols) return fail(EP_ERR_SHAPE, "row_stride %lld below num_cols %d", (long long)row_stride, num_cols);
+  if (num_rows >= ((int64_t)1 << 31) / kQuantThreads || num_cols > EP_MAX_QUANT_COLS || row_stride > ((int64_t)1 << 40))
+    return fail(EP_ERR_OVERFLOW, "%lld rows of %d (stride %lld): too large", (long long)num_rows, num_cols,
+                (long long)row_stride);
+  if (!x || !codes || !scales) return fail(EP_ERR_NULL, "x / codes / scales is NULL");
+  if (misaligned(x, type_bytes(type)) || misaligned(scales, 4))
+    return fail(EP_ERR_SHAPE, "x / scales must be aligned to their element size");
+  QuantArgs a{x, row_stride, codes, scales, num_rows, num_cols};
+  return with_type(type, [&](auto io) { return launch_quantize<decltype(io)>(a, (hipStream_t)stream); });
+}
+
+ep_status ep_expert_rows(const ep_handle* h, int64_t* row_start, int32_t* row_count, void* stream) {
+  ep_status st = check_handle(h);
+  if (st == EP_OK) st = check_device(h);
+  if (st != EP_OK) return st;
+  if (!row_start || !row_count) return fail(EP_ERR_NULL, "row_start / row_count is NULL");
+  if (misaligned(row_start, 8) || misaligned(row_count, 4))
+    return fail(EP_ERR_SHAPE, "row_start must be 8-byte aligned, row_count 4-byte aligned");
+  const LayoutDims& d = h->dims;
+  expert_rows_kernel<<<(d.E + 255) / 256, 256, 0, (hipStream_t)stream>>>(h->window_row_base, h->expert_offset, h->n_e,
+                                                                        d.E, d.El, d.cap, row_start, row_count);
+  EP_LAUNCHED("expert_rows_kernel");
+  return EP_OK;
+}
+
+ep_status ep_matmul_int8(const int8_t* a, const float* a_scale, int64_t num_rows, const int8_t* w,
+                         const float* w_scale, int32_t num_groups, const int64_t* row_start,
+                         const int32_t* row_count, int32_t inner, int32_t outer, uint32_t flags, int32_t out_type,
+                         void* out, void* stream) {
+  if (flags & ~(uint32_t)EP_MATMUL_GATED) return fail(EP_ERR_SHAPE, "unknown matmul flags 0x%x", flags);
+  if (out_type != EP_TYPE_F32 && out_type != EP_TYPE_BF16 && out_type != EP_TYPE_F16)
+    return fail(EP_ERR_SHAPE, "unknown element type %d", out_type);
+  const bool gated = flags & EP_MATMUL_GATED;
+  if (num_rows < 0 || num_groups < 0 || num_groups > EP_MAX_EXPERTS)
+    return fail(EP_ERR_SHAPE, "bad sizes: %lld rows, %d groups (at most %d)", (long long)num_rows, num_groups,
+                EP_MAX_EXPERTS);
+  if (inner < 16 || inner % 16 != 0 || inner > EP_MAX_MATMUL_INNER)
+    return fail(EP_ERR_SHAPE, "inner %d must be a multiple of 16 in [16, %d]", inner, EP_MAX_MATMUL_INNER);
+  if (outer < 1 || outer > EP_MAX_MATMUL_OUTER || (gated && outer % 2 != 0))
+    return fail(EP_ERR_SHAPE, "outer %d must lie in [1, %d] and be even for a gated product", outer, EP_MAX_MATMUL_OUTER);
+  if (num_rows >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "num_rows %lld reaches 2^31", (long long)num_rows);
+  if (num_rows == 0) return EP_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return fail(EP_ERR_NULL, "a / a_scale / w / w_scale / out is NULL");
+  if (num_groups > 0 && (!row_start || !row_count)) return fail(EP_ERR_NULL, "row_start / row_count is NULL");
+  if (misaligned(a, 16) || misaligned(w, 16) || misaligned(out, 16) || misaligned(a_scale, 4) ||
+      misaligned(w_scale, 4) || misaligned(row_start, 8) || misaligned(row_count, 4))
+    return fail(EP_ERR_SHAPE, "a / w / out must be 16-byte aligned, other arrays aligned to their element size");
+  MatmulArgs m{a, a_scale, w, w_scale, num_groups > 0 ? row_start : nullptr, num_groups > 0 ? row_count : nullptr,
+               out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer};
+  return with_type(out_type, [&](auto io) {
+    return gated ? launch_matmul<decltype(io), true>(m, (hipStream_t)stream)
+                 : launch_matmul<decltype(io), false>(m, (hipStream_t)stream);
+  });
 }
 
 void ep_handle_free(ep_handle* h) { release(h); }

@@ -63,12 +63,16 @@
 extern "C" {
 #endif
 
-#define EP_ABI_VERSION 4
+#define EP_ABI_VERSION 5
 
 /* Limits of the library. */
 #define EP_MAX_RANKS 1024
 #define EP_MAX_EXPERTS 4096
 #define EP_MAX_TOPK 32
+#define EP_MAX_ROUTE_GROUPS 64
+#define EP_MAX_QUANT_COLS (1 << 24)
+#define EP_MAX_MATMUL_INNER 131056 /* 128 * 128 * inner stays below 2^31 */
+#define EP_MAX_MATMUL_OUTER (1 << 20)
 
 typedef enum {
   EP_OK = 0,
@@ -307,6 +311,121 @@ ep_status ep_dispatch_prequant_cached(const ep_handle *h, uint32_t flags, const 
  */
 ep_status ep_combine(const ep_handle *h, const void *y, const float *topk_weights, const void *bias,
                      void *out, void *stream);
+
+/* --------------------------------------------------------------------------
+ * Routing and the experts' int8 products: what stands before ep_get_layout and
+ * between ep_dispatch and ep_combine.  None of these calls allocates, waits on
+ * the host or keeps state; all can be captured into a graph.  Apart from
+ * ep_expert_rows they take no handle and run on the current device, which has
+ * to be the one that `stream` and the arrays belong to.  No output may overlap
+ * an input or another output.
+ */
+
+/* Element types of the arrays given as `const void *`. */
+enum { EP_TYPE_F32 = 0, EP_TYPE_BF16 = 1, EP_TYPE_F16 = 2 };
+
+enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 };
+enum { EP_GROUP_MAX = 0, EP_GROUP_TOP2 = 1 };
+
+typedef struct {
+  int32_t num_experts; /* E, 1..EP_MAX_EXPERTS                                              */
+  int32_t num_topk;    /* K, 1..EP_MAX_TOPK, at most topk_groups * E / num_groups            */
+  int32_t num_groups;  /* G, 1..EP_MAX_ROUTE_GROUPS groups of E / G consecutive experts      */
+  int32_t topk_groups; /* groups that a token may choose from, 1..G                          */
+  int32_t score;       /* EP_SCORE_*                                                        */
+  int32_t group_score; /* EP_GROUP_*: a group's largest key, or the sum of its two largest   */
+  int32_t renormalize; /* != 0: the weights of a token are divided by their sum              */
+  float scale;         /* finite; multiplies the weights                                     */
+} ep_route_config;
+
+/* ep_route -- the router of every token: topk_idx and topk_weights as
+ * ep_get_layout, ep_dispatch and ep_combine take them (the tutorial's top-k
+ * gate that produces them, TileLang tutorial ch. 38, section 9).
+ *
+ *   logits        device, [num_tokens, E] of `type`, rows row_stride elements apart.
+ *   bias          device, fp32 [E], or NULL: added to the scores for the choice
+ *                 only (balance), not to the weights.
+ *   token_mask    device, u8 [num_tokens], or NULL: 0 leaves a token unrouted
+ *                 (a padded batch): ids -1, weights 0.
+ *   topk_idx      device, int64 [num_tokens, K].
+ *   topk_weights  device, fp32 [num_tokens, K].
+ * s = softmax(x) or sigmoid(x); key = s + bias.  The topk_groups groups of the
+ * largest group score are kept, and of their experts the K of the largest key,
+ * in falling order; ties go to the lowest index.  Order and ties are those of
+ * the keys in 64-bit arithmetic (of the logits themselves where neither a bias
+ * nor a sum of scores enters), so scores that fp32 cannot tell apart are still
+ * ordered.  weight = s of the choice, divided by the sum over the token's
+ * choices with renormalize, times scale; the quotient is formed from scores
+ * relative to the token's largest, so it holds also where s underflows.
+ * An expert whose logit is -Inf or NaN, or whose key is -Inf or NaN, is never
+ * chosen, and -Inf has score 0.  +Inf counts as the largest finite logit.  A
+ * group without a choosable expert comes last; the sum of a group with one
+ * choosable expert is that one's key.  A token with fewer than K choosable
+ * experts has ids -1 and weights 0 in its last slots.  A row holding NaN gets
+ * NaN weights (with its ids valid), so that the fault stays visible.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
+ep_status ep_route(const ep_route_config *cfg, int32_t type, const void *logits, int64_t num_tokens,
+                   int64_t row_stride, const float *bias, const uint8_t *token_mask, int64_t *topk_idx,
+                   float *topk_weights, void *stream);
+
+/* ep_route_backward -- gradient of the logits from that of the weights.
+ *   topk_idx      device, int64 [num_tokens, K], as ep_route gave them; an id
+ *                 outside [0, E) is an unused slot, an id that a token names
+ *                 twice gets the sum of both slots.
+ *   grad_weights  device, fp32 [num_tokens, K].
+ *   grad_logits   device, [num_tokens, E] contiguous, of `type`; every element
+ *                 is written (0 where nothing reaches a logit).
+ * The choice itself has no gradient, and neither has the bias, which enters
+ * nothing else.  num_groups, topk_groups and group_score are checked and not
+ * used.  Errors as ep_route. */
+ep_status ep_route_backward(const ep_route_config *cfg, int32_t type, const void *logits, int64_t num_tokens,
+                            int64_t row_stride, const int64_t *topk_idx, const float *grad_weights,
+                            void *grad_logits, void *stream);
+
+/* ep_quantize_int8 -- rows to int8 codes with one scale a row (activations: a
+ * token; weights: an output channel).
+ *   x       device, [num_rows, num_cols] of `type`, rows row_stride elements apart.
+ *   codes   device, int8 [num_rows, num_cols] contiguous.
+ *   scales  device, fp32 [num_rows].
+ * scale = amax / 127 in fp32; code = the whole number nearest to x / scale
+ * (exact quotient, ties to even), within +-127.  A row of zeros has scale 0 and
+ * codes 0 (so has one whose scale is below the smallest fp32 value); a row
+ * holding NaN or an infinity has scale 0x7FC00000 (NaN) and codes 0.
+ * The codes and scales can be dispatched with ep_dispatch_prequant, which
+ * copies any bytes: the scale repeated for every 128 channels, and with
+ * EP_DISPATCH_SCALES_COL_MAJOR the first row of recv_scales is the scale of
+ * every expanded row.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
+ep_status ep_quantize_int8(int32_t type, const void *x, int64_t num_rows, int32_t num_cols, int64_t row_stride,
+                           int8_t *codes, float *scales, void *stream);
+
+/* ep_expert_rows -- the rows of each expert in the handle's expanded tensors:
+ *   row_start  device, int64 [E]; row_count  device, int32 [E].
+ * Rows [start, start + count) are the expert's rows without its padding; in
+ * fixed mode only those kept in the window.  Enqueued on `stream`, nothing is
+ * read back.  Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_HANDLE_MISMATCH, EP_ERR_HIP. */
+ep_status ep_expert_rows(const ep_handle *h, int64_t *row_start, int32_t *row_count, void *stream);
+
+/* ep_matmul_int8 -- int8 rows times int8 weights, one weight matrix for all
+ * rows (num_groups 0) or one for the rows of each group (expert).
+ *   a          device, int8 [num_rows, inner];  a_scale  fp32 [num_rows].
+ *   w          device, int8 [num_groups, outer, inner] ([outer, inner] if
+ *              num_groups is 0);  w_scale  fp32 [num_groups, outer].
+ *   row_start, row_count  device, [num_groups] as ep_expert_rows gives them;
+ *              not used if num_groups is 0.  Groups must not overlap.  A range
+ *              is cut to the rows that exist; one that starts outside them is empty.
+ *   out        device, [num_rows, outer] of out_type; with EP_MATMUL_GATED
+ *              [num_rows, outer / 2].  Rows of no group are left as they were.
+ * y[r][n] = (sum_k a[r][k] * w[g][n][k]) * a_scale[r] * w_scale[g][n], the sum
+ * exact in int32, the scales in fp32, rounded once to out_type.  With
+ * EP_MATMUL_GATED out[r][n] = silu(y[r][n]) * y[r][n + outer / 2], also from
+ * fp32: neither half is rounded before.  inner is a multiple of 16.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
+#define EP_MATMUL_GATED 1u
+ep_status ep_matmul_int8(const int8_t *a, const float *a_scale, int64_t num_rows, const int8_t *w,
+                         const float *w_scale, int32_t num_groups, const int64_t *row_start,
+                         const int32_t *row_count, int32_t inner, int32_t outer, uint32_t flags, int32_t out_type,
+                         void *out, void *stream);
 
 /* ep_handle_free -- waits for the handle's own layout work, then releases its
  * device and pinned host memory.  The caller guarantees no other call using
