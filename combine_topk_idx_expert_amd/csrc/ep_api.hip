@@ -18,6 +18,7 @@
 #include "ep_mi355x.h"
 #include "ep_dispatch.hpp"
 #include "ep_int8.hpp"
+#include "ep_int8_tile.hpp"
 #include "ep_layout.hpp"
 #include "ep_route.hpp"
 

@@ -73,8 +73,22 @@ ep_status launch_quantize(const QuantArgs& a, hipStream_t s) {
   return EP_OK;
 }
 
+template <typename IO, bool GATED, int BM, int BN, int WM, int WN>
+ep_status launch_matmul_tile(const MatmulArgs& a, int per_cu, hipStream_t s) {
+  typedef TileShape<BM, BN, WM, WN> S;
+  const int bc = GATED ? BN / 2 : BN;
+  const int64_t n_tiles = (a.width + bc - 1) / bc;
+  const int64_t most = (a.M / BM + a.G) * n_tiles;  // each group's last row tile may be partly filled
+  if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "product of %lld tiles is too large", (long long)most);
+  const int grid = (int)std::min<int64_t>(most, 256 * per_cu);
+  matmul_tile_kernel<IO, GATED, BM, BN, WM, WN><<<grid, S::kThreads, S::lds(a.G), s>>>(a, (int)n_tiles);
+  EP_LAUNCHED("matmul_tile_kernel");
+  return EP_OK;
+}
+
 template <typename IO, bool GATED>
 ep_status launch_matmul(const MatmulArgs& a, hipStream_t s) {
+  if (a.M >= (int64_t)96 * a.G) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4>(a, 1, s);
   const int64_t nb = (a.width + 63) / 64;
   const int64_t tiles = (a.M + kRowTile - 1) / kRowTile;
   const int z = (int)std::min<int64_t>(a.row_start ? (tiles + a.G - 1) / a.G : tiles, 4096);

@@ -45,6 +45,9 @@ struct F32 {
   typedef float type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((float*)p)[i] = v; }
+  static __device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
+    *(u32x4*)((float*)p + i) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+  }
 };
 struct Bf16 {
   typedef uint16_t type;
@@ -54,11 +57,18 @@ struct Bf16 {
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
     ((uint16_t*)p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
   }
+  static __device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
+    *(u32x2*)((uint16_t*)p + i) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
 };
 struct F16 {
   typedef uint16_t type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((_Float16*)p)[i] = (_Float16)v; }
+  static __device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    *(f16x4*)((_Float16*)p + i) = f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+  }
 };
 
 constexpr float kNegInf = -__builtin_inff();
