@@ -782,7 +782,7 @@ ep_status ep_matmul_int8(const int8_t* a, const float* a_scale, int64_t num_rows
       misaligned(w_scale, 4) || misaligned(row_start, 8) || misaligned(row_count, 4))
     return fail(EP_ERR_SHAPE, "a / w / out must be 16-byte aligned, other arrays aligned to their element size");
   MatmulArgs m{a, a_scale, w, w_scale, num_groups > 0 ? row_start : nullptr, num_groups > 0 ? row_count : nullptr,
-               out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer};
+               out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer, 0, num_rows};
   return with_type(out_type, [&](auto io) {
     return gated ? launch_matmul<decltype(io), true>(m, (hipStream_t)stream)
                  : launch_matmul<decltype(io), false>(m, (hipStream_t)stream);

@@ -73,26 +73,82 @@ ep_status launch_quantize(const QuantArgs& a, hipStream_t s) {
   return EP_OK;
 }
 
-template <typename IO, bool GATED, int BM, int BN, int WM, int WN>
-ep_status launch_matmul_tile(const MatmulArgs& a, int per_cu, hipStream_t s) {
+constexpr int kCUs = 256;  // MI355X
+
+template <typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
+ep_status launch_matmul_tile(const MatmulArgs& a, hipStream_t s) {
   typedef TileShape<BM, BN, WM, WN> S;
   const int bc = GATED ? BN / 2 : BN;
   const int64_t n_tiles = (a.width + bc - 1) / bc;
   const int64_t most = (a.M / BM + a.G) * n_tiles;  // each group's last row tile may be partly filled
   if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "product of %lld tiles is too large", (long long)most);
-  const int grid = (int)std::min<int64_t>(most, 256 * per_cu);
-  matmul_tile_kernel<IO, GATED, BM, BN, WM, WN><<<grid, S::kThreads, S::lds(a.G), s>>>(a, (int)n_tiles);
+  const int grid = (int)std::min<int64_t>(most, kCUs);
+  matmul_tile_kernel<IO, GATED, BM, BN, WM, WN, HALVES><<<grid, S::kThreads, S::lds(a.G), s>>>(a, (int)n_tiles);
   EP_LAUNCHED("matmul_tile_kernel");
   return EP_OK;
 }
 
-template <typename IO, bool GATED>
-ep_status launch_matmul(const MatmulArgs& a, hipStream_t s) {
-  if (a.M >= (int64_t)96 * a.G) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4>(a, 1, s);
-  const int64_t nb = (a.width + 63) / 64;
-  const int64_t tiles = (a.M + kRowTile - 1) / kRowTile;
-  const int z = (int)std::min<int64_t>(a.row_start ? (tiles + a.G - 1) / a.G : tiles, 4096);
-  matmul_rows_kernel<IO, GATED><<<dim3((unsigned)nb, a.G, z), 256, 0, s>>>(a);
-  EP_LAUNCHED("matmul_rows_kernel");
+template <typename IO, bool GATED, int MT, int NT, int KW, int S>
+ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
+  const int bc = (GATED ? NT / 2 : NT) * 16;
+  const int64_t nb = (a.width + bc - 1) / bc;
+  const int64_t rows = a.row_start ? std::min(a.M, a.most) : a.M;
+  const int y = (int)std::min<int64_t>((rows + 16 * MT - 1) / (16 * MT), 4096);
+  matmul_split_kernel<IO, GATED, MT, NT, KW, S><<<dim3((unsigned)nb, y, a.G), KW * kWave, 0, s>>>(a);
+  EP_LAUNCHED("matmul_split_kernel");
   return EP_OK;
+}
+
+// Which kernel (both sides measured on MI355X):
+//  - tiles of 256 x 256 once they fill three quarters of the CUs; below that
+//    tiles of 128 x 256 while they fill three eighths (2048 x 7168 x 4096 gated: 67
+//    against 82 us; 8192 x 8192 x 8192: 256 x 256 by 10%);
+//  - below that, or for at most 64 rows, the split over the inner size (512 x 7168
+//    x 4096 gated: 29 us against 54 and 79; 64 rows: 11 against 44 and 49).
+//    Row tiles of 16, 32 or 64 by the rows there are.  Two waves a workgroup leave
+//    room for several workgroups a CU; four are better where the inner size is long
+//    and the grid at most one workgroup a CU (one row: 11 against 17 us), or one row tile of 16 (32
+//    groups of 3 rows, inner 7168: 150 against 155 us; inner 1024: 97 against 82).
+// Groups: their sizes are on the device.  A group of at most kFewRows rows is
+// the split's and a larger one the tiles'; each launch passes over the others'
+// groups.  No second launch where large groups cannot be many enough to fill the
+// tiles' grid (8 groups of 64 rows, 4096 x 2048: 19 against 47 us), nor a first
+// one where the mean is so large that few groups are small.
+constexpr int64_t kFewRows = 64;
+
+template <typename IO, bool GATED>
+ep_status launch_matmul_few(const MatmulArgs& a, int64_t mean, hipStream_t s) {
+  if (mean <= 16)
+    return a.K >= 2048 ? launch_matmul_split<IO, GATED, 1, 4, 4, 2>(a, s)
+                       : launch_matmul_split<IO, GATED, 1, 4, 2, 2>(a, s);
+  if (mean <= 32) return launch_matmul_split<IO, GATED, 2, 4, 2, 2>(a, s);
+  const int64_t blocks = (a.M + 63) / 64 * ((a.width + 31) / 32);
+  if (a.K >= 4096 && blocks <= kCUs) return launch_matmul_split<IO, GATED, 4, 4, 4, 2>(a, s);
+  return launch_matmul_split<IO, GATED, 4, 4, 2, 2>(a, s);
+}
+
+template <typename IO, bool GATED>
+ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
+  const int bc = GATED ? 128 : 256;
+  const int64_t n_tiles = (a.width + bc - 1) / bc;
+  a.least = 0;
+  a.most = a.M;
+  if (!a.row_start) {
+    if ((a.M + 255) / 256 * n_tiles >= 3 * kCUs / 4) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
+    if (a.M > kFewRows && (a.M + 127) / 128 * n_tiles >= 3 * kCUs / 8)
+      return launch_matmul_tile<IO, GATED, 128, 256, 2, 4, false>(a, s);
+    return launch_matmul_few<IO, GATED>(a, a.M, s);
+  }
+  const int64_t mean = a.M / a.G;
+  const int64_t large = std::min<int64_t>(a.G, a.M / (kFewRows + 1));
+  if ((a.M / 256 + large) * n_tiles < 3 * kCUs / 8) return launch_matmul_few<IO, GATED>(a, mean, s);
+  if (mean < 4 * kFewRows) {
+    MatmulArgs few = a;
+    few.most = kFewRows;
+    const ep_status st = launch_matmul_few<IO, GATED>(few, mean, s);
+    if (st != EP_OK) return st;
+    a.least = kFewRows + 1;
+  }
+  if ((a.M / 256 + a.G) * n_tiles >= 3 * kCUs / 4) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
+  return launch_matmul_tile<IO, GATED, 128, 256, 2, 4, false>(a, s);
 }

@@ -45,8 +45,11 @@ struct F32 {
   typedef float type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((float*)p)[i] = v; }
-  static __device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
-    *(u32x4*)((float*)p + i) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+  // eight values to an address that is a multiple of 16 bytes
+  static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    *(f32x4*)((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
+    *(f32x4*)((float*)p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
   }
 };
 struct Bf16 {
@@ -57,17 +60,19 @@ struct Bf16 {
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
     ((uint16_t*)p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
   }
-  static __device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
-    *(u32x2*)((uint16_t*)p + i) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
+    *(u32x4*)((uint16_t*)p + i) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                        pack_bf16x2(v[6], v[7])};
   }
 };
 struct F16 {
   typedef uint16_t type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((_Float16*)p)[i] = (_Float16)v; }
-  static __device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    *(f16x4*)((_Float16*)p + i) = f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+  static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    *(f16x8*)((_Float16*)p + i) = f16x8{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3],
+                                        (_Float16)v[4], (_Float16)v[5], (_Float16)v[6], (_Float16)v[7]};
   }
 };
 
