@@ -48,8 +48,36 @@ ep_status validate_route(const ep_route_config* c, int32_t type, int64_t num_tok
   return EP_OK;
 }
 
+template <typename IO, int LPR, int VPL>
+ep_status launch_route_lanes(const RouteArgs& a, RouteLanes p, hipStream_t s) {
+  p.pitch = 4 * ((p.seg + 3) / 4 | 1);
+  p.magic = (1 << 20) / p.seg + 1;
+  constexpr int V = sizeof(typename IO::type) == 4 ? 4 : 8;
+  p.vec = p.seg % V == 0 && a.E % V == 0 && a.stride % V == 0 && !misaligned(a.logits, 16);
+  constexpr int kRows = kWave / LPR;
+  const size_t lds = std::max((size_t)kWave * p.pitch * sizeof(float), (size_t)a.E * sizeof(double));
+  route_lanes_kernel<IO, LPR, VPL><<<(a.T + kRows - 1) / kRows, kWave, lds, s>>>(a, p);
+  EP_LAUNCHED("route_lanes_kernel");
+  return EP_OK;
+}
+
+// Up to 512 experts and 8 choices: several rows a wave.  Lanes own whole shares
+// of groups (a group is 1, 2, 4 or 8 lanes); routers for which that does not
+// come out, and wider ones, take one row a wave.
 template <typename IO>
 ep_status launch_route(const RouteArgs& a, hipStream_t s) {
+  if (a.K <= 8 && a.E <= 512) {
+    const int lanes = a.E <= 256 ? 8 : 16, gs = a.E / a.G;
+    RouteLanes p{};
+    for (p.wide = 1; p.wide <= 8; p.wide *= 2) {
+      p.seg = a.G == 1 ? (a.E + lanes - 1) / lanes : gs / p.wide;
+      if (a.G > 1 && (gs % p.wide != 0 || a.G * p.wide > lanes || p.seg > 32)) continue;
+      if (lanes == 16) return launch_route_lanes<IO, 16, 32>(a, p, s);
+      if (p.seg <= 8) return launch_route_lanes<IO, 8, 8>(a, p, s);
+      if (p.seg <= 16) return launch_route_lanes<IO, 8, 16>(a, p, s);
+      return launch_route_lanes<IO, 8, 32>(a, p, s);
+    }
+  }
   const int waves = a.E > 2048 ? kRouteWaves / 2 : kRouteWaves;  // at most 64 KiB of LDS
   const int blocks = (a.T + waves - 1) / waves;
   route_kernel<IO><<<blocks, waves * kWave, (size_t)waves * a.E * sizeof(double), s>>>(a);

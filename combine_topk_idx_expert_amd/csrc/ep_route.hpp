@@ -45,6 +45,10 @@ struct F32 {
   typedef float type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((float*)p)[i] = v; }
+  static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+  }
   // eight values to an address that is a multiple of 16 bytes
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -60,6 +64,13 @@ struct Bf16 {
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
     ((uint16_t*)p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
   }
+  static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     *(u32x4*)((uint16_t*)p + i) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                         pack_bf16x2(v[6], v[7])};
@@ -69,6 +80,13 @@ struct F16 {
   typedef uint16_t type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((_Float16*)p)[i] = (_Float16)v; }
+  static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)w[i]);
+      f[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] >> 16));
+    }
+  }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
     *(f16x8*)((_Float16*)p + i) = f16x8{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3],
@@ -226,6 +244,353 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / kWave) + wave;
   if (row >= a.T) return;
   route_row<IO>(a, row, route_lds + (size_t)wave * a.E);
+}
+
+// --------------------------------------------------------------------------
+// Several rows a wave: LPR lanes share a row of at most LPR * VPL experts and
+// K <= 8 choices.  Lane l owns experts l * seg .. l * seg + seg - 1, brought to
+// its registers through LDS (memory is read in whole lines).
+//
+// Keys are fp32 and carry their expert in the low bits of a double (a converted
+// float leaves 29 mantissa bits free), so that one v_max_f64 and one v_min_f64
+// exchange key and expert, and equal keys stand in the order of the experts.  A
+// lane sorts eights of its keys, keeps the best eight, and three or four
+// bitonic merges over its neighbours leave the row's best eight in every lane.
+//
+// The definition orders the keys by their exact values.  Logits are exact.
+// Scores are not: a row where two neighbours among the choices, the last choice
+// and the best expert left out, or a kept and a dropped group, lie within the
+// error of the fp32 scores (and are not equal for being made of equal numbers)
+// is done over in 64 bits by the whole wave (route_row), about one row in 500.
+
+// Value of lane (lane ^ X), X < 16, by DPP.
+template <int X>
+__device__ __forceinline__ int xor_lane(int v) {
+  if constexpr (X >= 8) return xor_lane<15 ^ X>(__builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, false));  // mirror of 16
+  else if constexpr (X >= 4) return xor_lane<7 ^ X>(__builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false));  // mirror of 8
+  else if constexpr (X == 3) return __builtin_amdgcn_update_dpp(0, v, 0x1B, 0xF, 0xF, false);
+  else if constexpr (X == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false);
+  else if constexpr (X == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
+  else return v;
+}
+template <int X>
+__device__ __forceinline__ float xor_lane(float v) { return __int_as_float(xor_lane<X>(__float_as_int(v))); }
+template <int X>
+__device__ __forceinline__ double xor_lane(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)xor_lane<X>((int)(uint32_t)b) |
+                                        (uint64_t)(uint32_t)xor_lane<X>((int)(uint32_t)(b >> 32)) << 32);
+}
+
+// Over the N (8 or 16) lanes of a row; every lane gets the result.
+template <int N>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, xor_lane<1>(v));
+  v = fmaxf(v, xor_lane<2>(v));
+  v = fmaxf(v, xor_lane<7>(v));
+  if (N == 16) v = fmaxf(v, xor_lane<15>(v));
+  return v;
+}
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += xor_lane<1>(v);
+  v += xor_lane<2>(v);
+  v += xor_lane<7>(v);
+  if (N == 16) v += xor_lane<15>(v);
+  return v;
+}
+template <int N>
+__device__ __forceinline__ int lanes_sum(int v) {
+  v += xor_lane<1>(v);
+  v += xor_lane<2>(v);
+  v += xor_lane<7>(v);
+  if (N == 16) v += xor_lane<15>(v);
+  return v;
+}
+
+__device__ __forceinline__ void exchange(double& a, double& b) {  // the larger first
+  const double hi = fmax(a, b), lo = fmin(a, b);
+  a = hi;
+  b = lo;
+}
+__device__ __forceinline__ void sort8(double (&v)[8]) {
+  exchange(v[0], v[2]); exchange(v[1], v[3]); exchange(v[4], v[6]); exchange(v[5], v[7]);
+  exchange(v[0], v[4]); exchange(v[1], v[5]); exchange(v[2], v[6]); exchange(v[3], v[7]);
+  exchange(v[0], v[1]); exchange(v[2], v[3]); exchange(v[4], v[5]); exchange(v[6], v[7]);
+  exchange(v[2], v[4]); exchange(v[3], v[5]);
+  exchange(v[1], v[4]); exchange(v[3], v[6]);
+  exchange(v[1], v[2]); exchange(v[3], v[4]); exchange(v[5], v[6]);
+}
+// The best eight of two falling lists of eight, falling.
+__device__ __forceinline__ void merge8(double (&v)[8], const double (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fmax(v[i], o[7 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) exchange(v[i], v[i + d]);
+}
+template <int X>
+__device__ __forceinline__ void merge8_lane(double (&v)[8]) {
+  double o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = xor_lane<X>(v[i]);
+  merge8(v, o);
+}
+
+struct RouteLanes {
+  int seg;      // experts of a lane
+  int pitch;    // floats between lanes in LDS: a multiple of 4, odd in 16-byte units
+  int magic;    // e / seg == (e * magic) >> 20 for e < 1024
+  int wide;     // lanes of a group
+  int vec;      // rows can be read 16 bytes at a time, each chunk within one lane's experts
+};
+
+// log2(e) * x for exp2, and the hardware's exp2 and reciprocal: the scores of
+// the first pass, whose errors the margins below bound.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+template <typename IO, int LPR, int VPL>
+__global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLanes p) {
+  constexpr int kRows = kWave / LPR;
+  extern __shared__ float lanes_lds[];  // [64][pitch]
+  const int lane = threadIdx.x;
+  const int l = lane % LPR;
+  const int64_t row0 = (int64_t)blockIdx.x * kRows;
+  const int64_t row = min(row0 + lane / LPR, (int64_t)a.T - 1);
+  const int64_t base = row * a.stride;
+  float* const mine = lanes_lds + lane * p.pitch;
+  float* const row_lds = lanes_lds + (lane - l) * p.pitch;
+  const bool by_logit = !a.bias && (a.G == 1 || !a.top2);
+
+  // logits to LDS
+  constexpr int V = sizeof(typename IO::type) == 4 ? 4 : 8;
+  if (p.vec) {
+    constexpr int kChunks = (VPL + V - 1) / V;
+    u32x4 raw[kChunks];
+    const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+    const int chunks = a.E / V;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int c = j * LPR + l;
+      raw[j] = c < chunks ? src[c] : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int c = j * LPR + l;
+      if (c < chunks) {
+        const int e = c * V, o = (e * p.magic) >> 20;
+        float* dst = row_lds + o * p.pitch + (e - o * p.seg);
+        float f[V];
+        IO::unpack(raw[j], f);
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          typedef float f32x4 __attribute__((ext_vector_type(4)));
+          *(f32x4*)(dst + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
+        }
+      }
+    }
+  } else {
+    for (int e = l; e < a.E; e += LPR) {
+      const int o = (e * p.magic) >> 20;
+      row_lds[o * p.pitch + (e - o * p.seg)] = IO::load(a.logits, base + e);
+    }
+  }
+  wave_sync();
+
+  // this lane's logits; kNegInf: cannot be chosen
+  const int e0 = l * p.seg;
+  const int have = max(0, min(p.seg, a.E - e0));
+  float key[VPL];
+  bool nan = false;
+  float top = kNegInf;
+#pragma unroll
+  for (int i = 0; i < VPL; i += 4) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    f32x4 v = {kNegInf, kNegInf, kNegInf, kNegInf};
+    if (i < p.seg) v = *(const f32x4*)(mine + i);  // seg is below the pitch, a multiple of 4
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x = i + j < have ? v[j] : kNegInf;
+      nan |= x != x;
+      x = x != x ? kNegInf : clean_logit(x);
+      top = fmaxf(top, x);
+      key[i + j] = x;
+    }
+  }
+  const uint64_t row_lanes = (LPR == 16 ? 0xFFFFull : 0xFFull) << (lane - l);
+  const bool any_nan = (ballot(nan) & row_lanes) != 0;
+  float total = 1.0f;
+  if (!a.sigmoid && (!by_logit || !a.renorm)) {
+    top = lanes_max<LPR>(top);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sum += key[i] > kNegInf ? fast_exp(key[i] - top) : 0.0f;
+    total = lanes_sum<LPR>(sum);
+  }
+  if (!by_logit) {
+    const float inv = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float x = key[i];
+      float k = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - top) * inv;
+      if (a.bias && i < have) k += a.bias[e0 + i];
+      // (a key of -Inf or NaN cannot be chosen; one of +Inf is decided in 64 bits)
+      key[i] = x > kNegInf && k > kNegInf ? fminf(k, 3.402823466e38f) : kNegInf;
+    }
+  }
+  // two keys of the row keep their order where they differ by more: twice the
+  // error of a score (sigmoid: exponent and two hardware operations, below
+  // 2^-22; softmax: the sum's error too, below 2^-18 of the largest score) and
+  // of the sum with the bias
+  const float margin0 = a.sigmoid ? 0x1p-20f : 0x1p-16f * __builtin_amdgcn_rcpf(total);
+  bool unsure = false;
+
+  if (a.G > 1) {
+    float m1 = kNegInf, m2 = kNegInf;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      m2 = fmaxf(m2, fminf(m1, key[i]));
+      m1 = fmaxf(m1, key[i]);
+    }
+    auto join = [&](float o1, float o2) {
+      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+      m1 = fmaxf(m1, o1);
+    };
+    // lanes of one group are neighbours: after each merge all of them agree
+    if (p.wide >= 2) join(xor_lane<1>(m1), xor_lane<1>(m2));
+    if (p.wide >= 4) join(xor_lane<2>(m1), xor_lane<2>(m2));
+    if (p.wide >= 8) join(xor_lane<7>(m1), xor_lane<7>(m2));
+    const float s = a.top2 && m2 > kNegInf ? m1 + m2 : m1;
+    const int g = l / p.wide;
+    int ahead = 0;
+    auto count = [&](float o, int ol) {
+      const int og = ol / p.wide;
+      ahead += ol % p.wide == 0 && og < a.G && og != g && (o > s || (o == s && og < g)) ? 1 : 0;
+    };
+    count(xor_lane<1>(s), l ^ 1);
+    count(xor_lane<2>(s), l ^ 2);
+    count(xor_lane<3>(s), l ^ 3);
+    count(xor_lane<4>(s), l ^ 4);
+    count(xor_lane<5>(s), l ^ 5);
+    count(xor_lane<6>(s), l ^ 6);
+    count(xor_lane<7>(s), l ^ 7);
+    if (LPR == 16) {
+      count(xor_lane<8>(s), l ^ 8);
+      count(xor_lane<9>(s), l ^ 9);
+      count(xor_lane<10>(s), l ^ 10);
+      count(xor_lane<11>(s), l ^ 11);
+      count(xor_lane<12>(s), l ^ 12);
+      count(xor_lane<13>(s), l ^ 13);
+      count(xor_lane<14>(s), l ^ 14);
+      count(xor_lane<15>(s), l ^ 15);
+    }
+    const bool kept = g < a.G && ahead < a.TG;
+    if (!by_logit) {
+      const float worst = -lanes_max<LPR>(kept ? -s : kNegInf);  // of the kept groups
+      const float best = lanes_max<LPR>(!kept && g < a.G ? s : kNegInf);
+      const float margin = (a.top2 ? 2.0f : 1.0f) * margin0 + 0x1p-21f * fmaxf(fabsf(worst), fabsf(best));
+      unsure |= best > kNegInf && !(worst - best > margin);
+    }
+    if (!kept)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = kNegInf;
+  }
+
+  double list[8];
+#pragma unroll
+  for (int c = 0; c < VPL; c += 8) {
+    double v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float k = key[c + i];
+      const int e = e0 + c + i;
+      const uint32_t tag = k > kNegInf ? (uint32_t)(k < 0.0f ? e : 4095 - e) : 0u;
+      v[i] = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)k) | tag);
+    }
+    sort8(v);
+    if (c == 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) list[i] = v[i];
+    else
+      merge8(list, v);
+  }
+  merge8_lane<1>(list);
+  merge8_lane<2>(list);
+  merge8_lane<7>(list);
+  if (LPR == 16) merge8_lane<15>(list);
+
+  // lane l < 8 of the row holds choice l
+  double mine_d = list[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mine_d = l == i ? list[i] : mine_d;
+  const bool chosen = l < a.K && mine_d > -__builtin_inf();
+  const uint32_t tag = (uint32_t)__builtin_bit_cast(uint64_t, mine_d) & 4095u;
+  const int e = chosen ? (int)(mine_d < 0.0 ? tag : 4095u - tag) : 0;
+  const int o = (e * p.magic) >> 20;
+  const float x = chosen ? clean_logit(row_lds[o * p.pitch + (e - o * p.seg)]) : kNegInf;
+
+  if (!by_logit) {
+    const float kf = chosen ? (float)mine_d : 0.0f;  // the tag is below half a step of fp32
+    const float b = a.bias && chosen ? a.bias[e] : 0.0f;
+    const float margin = margin0 + 0x1p-22f * lanes_max<LPR>(fabsf(kf));
+    // neighbours among the choices
+    const float k2 = __shfl_down(kf, 1, 64), x2 = __shfl_down(x, 1, 64), b2 = __shfl_down(b, 1, 64);
+    const bool next = __shfl_down((int)chosen, 1, 64) != 0 && l + 1 < a.K;
+    unsure |= chosen && next && !(kf - k2 > margin) && !(x == x2 && b == b2);
+    // the last choice against those left out
+    double last_d = list[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) last_d = a.K - 1 == i ? list[i] : last_d;
+    const bool full = last_d > -__builtin_inf();
+    const float last = (float)last_d;
+    int near = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) near += key[i] > kNegInf && !(last - key[i] > margin) ? 1 : 0;
+    near = lanes_sum<LPR>(near);
+    if (ballot(full && near > a.K)) {
+      const int at = lane - l + a.K - 1;
+      const float xk = __shfl(x, at, 64), bk = __shfl(b, at, 64);
+      int other = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (i >= have || !(key[i] > kNegInf) || last - key[i] > margin) continue;
+        other += clean_logit(mine[i]) == xk && (!a.bias || a.bias[e0 + i] == bk) ? 0 : 1;
+      }
+      other = lanes_sum<LPR>(other);
+      const int among = lanes_sum<LPR>(chosen && !(x == xk && b == bk) ? 1 : 0);
+      unsure |= full && other != among;
+    }
+  }
+
+  // weights, as route_row forms them
+  float w = 0.0f;
+  if (a.renorm) {
+    const float best = lanes_max<LPR>(x);
+    if (chosen) {
+      const float t = fminf(best, 0.0f);
+      w = !a.sigmoid ? expf(x - best) : x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - t) / (1.0f + expf(x));
+    }
+    const float sum = lanes_sum<LPR>(w);
+    if (chosen) w /= sum;
+  } else if (chosen) {
+    w = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - top) / total;
+  }
+  if (l < a.K && row0 + lane / LPR < a.T) {
+    const bool put = chosen && (!a.mask || a.mask[row] != 0);
+    a.idx[row * a.K + l] = put ? e : -1;
+    a.w[row * a.K + l] = !put ? 0.0f : any_nan ? __uint_as_float(0x7FC00000u) : w * a.scale;
+  }
+
+  // the rows whose order fp32 does not settle
+  uint64_t redo = ballot(unsure && row0 + lane / LPR < a.T);
+  if (redo) {
+    wave_sync();
+    for (int r = 0; r < kRows; ++r)
+      if ((redo >> (r * LPR)) & (LPR == 16 ? 0xFFFFull : 0xFFull))
+        route_row<IO>(a, row0 + r, (double*)lanes_lds);
+  }
 }
 
 // Gradient of the logits from the gradient g of the weights, one row a wave.
