@@ -54,6 +54,7 @@ ep_status launch_route_lanes(const RouteArgs& a, RouteLanes p, hipStream_t s) {
   p.magic = (1 << 20) / p.seg + 1;
   constexpr int V = sizeof(typename IO::type) == 4 ? 4 : 8;
   p.vec = p.seg % V == 0 && a.E % V == 0 && a.stride % V == 0 && !misaligned(a.logits, 16);
+  p.bias_vec = p.seg % 4 == 0 && a.E % 4 == 0 && !misaligned(a.bias, 16);
   constexpr int kRows = kWave / LPR;
   const size_t lds = std::max((size_t)kWave * p.pitch * sizeof(float), (size_t)a.E * sizeof(double));
   route_lanes_kernel<IO, LPR, VPL><<<(a.T + kRows - 1) / kRows, kWave, lds, s>>>(a, p);
@@ -69,9 +70,10 @@ ep_status launch_route(const RouteArgs& a, hipStream_t s) {
   if (a.K <= 8 && a.E <= 512) {
     const int lanes = a.E <= 256 ? 8 : 16, gs = a.E / a.G;
     RouteLanes p{};
-    for (p.wide = 1; p.wide <= 8; p.wide *= 2) {
-      p.seg = a.G == 1 ? (a.E + lanes - 1) / lanes : gs / p.wide;
-      if (a.G > 1 && (gs % p.wide != 0 || a.G * p.wide > lanes || p.seg > 32)) continue;
+    for (p.shift = 0; p.shift <= 3; ++p.shift) {
+      const int wide = 1 << p.shift;
+      p.seg = a.G == 1 ? (a.E + lanes - 1) / lanes : gs / wide;
+      if (a.G > 1 && (gs % wide != 0 || a.G * wide > lanes || p.seg > 32)) continue;
       if (lanes == 16) return launch_route_lanes<IO, 16, 32>(a, p, s);
       if (p.seg <= 8) return launch_route_lanes<IO, 8, 8>(a, p, s);
       if (p.seg <= 16) return launch_route_lanes<IO, 8, 16>(a, p, s);

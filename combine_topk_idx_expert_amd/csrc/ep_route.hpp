@@ -251,11 +251,13 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // K <= 8 choices.  Lane l owns experts l * seg .. l * seg + seg - 1, brought to
 // its registers through LDS (memory is read in whole lines).
 //
-// Keys are fp32 and carry their expert in the low bits of a double (a converted
-// float leaves 29 mantissa bits free), so that one v_max_f64 and one v_min_f64
-// exchange key and expert, and equal keys stand in the order of the experts.  A
-// lane sorts eights of its keys, keeps the best eight, and three or four
-// bitonic merges over its neighbours leave the row's best eight in every lane.
+// Keys are fp32.  A key's bits are taken as the high word of a double, whose
+// order is that of the floats (all of them finite doubles, -Inf included), with
+// the expert in the low word (inverted for positive keys): one v_max_f64 and one
+// v_min_f64 exchange key and expert, and equal keys stand in the order of the
+// experts.  (Scores skip the inversion by sign, two operations a key: a row whose
+// last choice has a negative key is done over.)  A lane sorts eights of its keys, keeps the best eight, and three or
+// four bitonic merges over its neighbours leave the row's best eight in every lane.
 //
 // The definition orders the keys by their exact values.  Logits are exact.
 // Scores are not: a row where two neighbours among the choices, the last choice
@@ -308,8 +310,21 @@ __device__ __forceinline__ int lanes_sum(int v) {
   return v;
 }
 
+// v_max_f64 and v_min_f64 as they are: fmax would first quiet operands that the
+// compiler cannot prove to be no signalling NaN (a third more instructions), and
+// the keys are none.
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
 __device__ __forceinline__ void exchange(double& a, double& b) {  // the larger first
-  const double hi = fmax(a, b), lo = fmin(a, b);
+  const double hi = max64(a, b), lo = min64(a, b);
   a = hi;
   b = lo;
 }
@@ -324,7 +339,7 @@ __device__ __forceinline__ void sort8(double (&v)[8]) {
 // The best eight of two falling lists of eight, falling.
 __device__ __forceinline__ void merge8(double (&v)[8], const double (&o)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fmax(v[i], o[7 - i]);
+  for (int i = 0; i < 8; ++i) v[i] = max64(v[i], o[7 - i]);
 #pragma unroll
   for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
@@ -334,17 +349,33 @@ __device__ __forceinline__ void merge8(double (&v)[8], const double (&o)[8]) {
 template <int X>
 __device__ __forceinline__ void merge8_lane(double (&v)[8]) {
   double o[8];
+  // two wait states between the writes above and the DPP reads
+  asm("s_nop 1" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]));
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = xor_lane<X>(v[i]);
   merge8(v, o);
+}
+
+// by_sign: -1, or 0 for ~e whatever the key
+__device__ __forceinline__ double tagged(float k, int e, int by_sign) {
+  const uint32_t hi = __float_as_uint(k);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | (uint32_t)(~e ^ (((int)hi >> 31) & by_sign)));
+}
+__device__ __forceinline__ float key_of(double d) {
+  return __uint_as_float((uint32_t)(__builtin_bit_cast(uint64_t, d) >> 32));
+}
+__device__ __forceinline__ int expert_of(double d, int by_sign) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, d);
+  return ~((int)(uint32_t)b ^ (((int)(uint32_t)(b >> 32) >> 31) & by_sign));
 }
 
 struct RouteLanes {
   int seg;      // experts of a lane
   int pitch;    // floats between lanes in LDS: a multiple of 4, odd in 16-byte units
   int magic;    // e / seg == (e * magic) >> 20 for e < 1024
-  int wide;     // lanes of a group
+  int shift;    // 1 << shift lanes of a group
   int vec;      // rows can be read 16 bytes at a time, each chunk within one lane's experts
+  int bias_vec; // so can the bias
 };
 
 // log2(e) * x for exp2, and the hardware's exp2 and reciprocal: the scores of
@@ -399,45 +430,85 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   }
   wave_sync();
 
-  // this lane's logits; kNegInf: cannot be chosen
+  // this lane's logits.  Rows of numbers alone, in whole shares, go straight on;
+  // where the wave has an infinity, a NaN or a lane with fewer experts than VPL,
+  // kNegInf marks what cannot be chosen.
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
   const int e0 = l * p.seg;
   const int have = max(0, min(p.seg, a.E - e0));
   float key[VPL];
-  bool nan = false;
-  float top = kNegInf;
+  float top = kNegInf, bottom = __builtin_inff();
 #pragma unroll
   for (int i = 0; i < VPL; i += 4) {
-    typedef float f32x4 __attribute__((ext_vector_type(4)));
     f32x4 v = {kNegInf, kNegInf, kNegInf, kNegInf};
     if (i < p.seg) v = *(const f32x4*)(mine + i);  // seg is below the pitch, a multiple of 4
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x = i + j < have ? v[j] : kNegInf;
-      nan |= x != x;
-      x = x != x ? kNegInf : clean_logit(x);
-      top = fmaxf(top, x);
-      key[i + j] = x;
-    }
+    for (int j = 0; j < 4; ++j) key[i + j] = v[j];
   }
-  const uint64_t row_lanes = (LPR == 16 ? 0xFFFFull : 0xFFull) << (lane - l);
-  const bool any_nan = (ballot(nan) & row_lanes) != 0;
-  float total = 1.0f;
-  if (!a.sigmoid && (!by_logit || !a.renorm)) {
-    top = lanes_max<LPR>(top);
-    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += key[i] > kNegInf ? fast_exp(key[i] - top) : 0.0f;
-    total = lanes_sum<LPR>(sum);
+  for (int i = 0; i < VPL; ++i) {
+    top = __builtin_elementwise_maximum(top, key[i]);  // NaN if one of them is
+    bottom = __builtin_elementwise_minimum(bottom, key[i]);
   }
-  if (!by_logit) {
-    const float inv = __builtin_amdgcn_rcpf(total);
+  const bool special = ballot(have < VPL || !(top < __builtin_inff()) || !(bottom > kNegInf)) != 0;
+  bool any_nan = false;
+  if (special) {
+    bool nan = false;
+    top = kNegInf;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const float x = key[i];
-      float k = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - top) * inv;
-      if (a.bias && i < have) k += a.bias[e0 + i];
-      // (a key of -Inf or NaN cannot be chosen; one of +Inf is decided in 64 bits)
-      key[i] = x > kNegInf && k > kNegInf ? fminf(k, 3.402823466e38f) : kNegInf;
+      const float x = i < have ? key[i] : kNegInf;
+      nan |= x != x;
+      key[i] = x != x ? kNegInf : clean_logit(x);
+      top = fmaxf(top, key[i]);
+    }
+    const uint64_t row_lanes = (LPR == 16 ? 0xFFFFull : 0xFFull) << (lane - l);
+    any_nan = (ballot(nan) & row_lanes) != 0;
+  }
+  float total = 1.0f;
+  if (!a.sigmoid && (!by_logit || !a.renorm)) {
+    top = fmaxf(lanes_max<LPR>(top), -3.402823466e38f);  // finite, also in a row without a choice
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sum += fast_exp(key[i] - top);  // 0 for kNegInf
+    total = lanes_sum<LPR>(sum);
+  }
+  if (by_logit) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] += 0.0f;  // -0 ties with +0
+  } else {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-key[i]));
+    } else {
+      const float inv = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = fast_exp(key[i] - top) * inv;
+    }
+    if (special) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = i < have && mine[i] > kNegInf ? key[i] : kNegInf;
+    }
+    if (a.bias) {
+      float best = kNegInf;
+      if (p.bias_vec) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) {
+          const f32x4 b = *(const f32x4*)(a.bias + (i < have ? e0 + i : 0));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) key[i + j] += b[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] += a.bias[i < have ? e0 + i : 0];
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) best = __builtin_elementwise_maximum(best, key[i]);
+      // a key of -Inf or NaN cannot be chosen; one of +Inf is decided in 64 bits
+      if (ballot(!(best < __builtin_inff()))) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = key[i] > kNegInf ? fminf(key[i], 3.402823466e38f) : kNegInf;
+      }
     }
   }
   // two keys of the row keep their order where they differ by more: twice the
@@ -459,15 +530,16 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       m1 = fmaxf(m1, o1);
     };
     // lanes of one group are neighbours: after each merge all of them agree
-    if (p.wide >= 2) join(xor_lane<1>(m1), xor_lane<1>(m2));
-    if (p.wide >= 4) join(xor_lane<2>(m1), xor_lane<2>(m2));
-    if (p.wide >= 8) join(xor_lane<7>(m1), xor_lane<7>(m2));
+    if (p.shift >= 1) join(xor_lane<1>(m1), xor_lane<1>(m2));
+    if (p.shift >= 2) join(xor_lane<2>(m1), xor_lane<2>(m2));
+    if (p.shift >= 3) join(xor_lane<7>(m1), xor_lane<7>(m2));
+    const int g = l >> p.shift;
+    // (groups past the last own nothing: -Inf, behind every other or tied with an empty one)
     const float s = a.top2 && m2 > kNegInf ? m1 + m2 : m1;
-    const int g = l / p.wide;
     int ahead = 0;
     auto count = [&](float o, int ol) {
-      const int og = ol / p.wide;
-      ahead += ol % p.wide == 0 && og < a.G && og != g && (o > s || (o == s && og < g)) ? 1 : 0;
+      const int og = ol >> p.shift;
+      ahead += (o > s) | ((o == s) & (og < g)) ? 1 : 0;
     };
     count(xor_lane<1>(s), l ^ 1);
     count(xor_lane<2>(s), l ^ 2);
@@ -486,35 +558,32 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       count(xor_lane<14>(s), l ^ 14);
       count(xor_lane<15>(s), l ^ 15);
     }
-    const bool kept = g < a.G && ahead < a.TG;
+    // every lane of a group ahead counted
+    const bool kept = g < a.G && (ahead >> p.shift) < a.TG;
     if (!by_logit) {
       const float worst = -lanes_max<LPR>(kept ? -s : kNegInf);  // of the kept groups
       const float best = lanes_max<LPR>(!kept && g < a.G ? s : kNegInf);
       const float margin = (a.top2 ? 2.0f : 1.0f) * margin0 + 0x1p-21f * fmaxf(fabsf(worst), fabsf(best));
       unsure |= best > kNegInf && !(worst - best > margin);
     }
-    if (!kept)
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = kNegInf;
+    for (int i = 0; i < VPL; ++i) key[i] = kept ? key[i] : kNegInf;
   }
 
+  const int by_sign = by_logit ? -1 : 0;
   double list[8];
 #pragma unroll
   for (int c = 0; c < VPL; c += 8) {
     double v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float k = key[c + i];
-      const int e = e0 + c + i;
-      const uint32_t tag = k > kNegInf ? (uint32_t)(k < 0.0f ? e : 4095 - e) : 0u;
-      v[i] = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)k) | tag);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = tagged(key[c + i], e0 + c + i, by_sign);
     sort8(v);
-    if (c == 0)
+    if (c == 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) list[i] = v[i];
-    else
+    } else {
       merge8(list, v);
+    }
   }
   merge8_lane<1>(list);
   merge8_lane<2>(list);
@@ -525,14 +594,14 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   double mine_d = list[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) mine_d = l == i ? list[i] : mine_d;
-  const bool chosen = l < a.K && mine_d > -__builtin_inf();
-  const uint32_t tag = (uint32_t)__builtin_bit_cast(uint64_t, mine_d) & 4095u;
-  const int e = chosen ? (int)(mine_d < 0.0 ? tag : 4095u - tag) : 0;
+  const bool chosen = l < a.K && key_of(mine_d) > kNegInf;
+  const int e = chosen ? expert_of(mine_d, by_sign) : 0;
   const int o = (e * p.magic) >> 20;
   const float x = chosen ? clean_logit(row_lds[o * p.pitch + (e - o * p.seg)]) : kNegInf;
 
   if (!by_logit) {
-    const float kf = chosen ? (float)mine_d : 0.0f;  // the tag is below half a step of fp32
+    unsure |= chosen && key_of(mine_d) < 0.0f;
+    const float kf = chosen ? key_of(mine_d) : 0.0f;
     const float b = a.bias && chosen ? a.bias[e] : 0.0f;
     const float margin = margin0 + 0x1p-22f * lanes_max<LPR>(fabsf(kf));
     // neighbours among the choices
@@ -543,11 +612,12 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     double last_d = list[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) last_d = a.K - 1 == i ? list[i] : last_d;
-    const bool full = last_d > -__builtin_inf();
-    const float last = (float)last_d;
+    const float last = key_of(last_d);
+    const bool full = last > kNegInf;
+    const float from = last - margin;
     int near = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) near += key[i] > kNegInf && !(last - key[i] > margin) ? 1 : 0;
+    for (int i = 0; i < VPL; ++i) near += key[i] >= from ? 1 : 0;
     near = lanes_sum<LPR>(near);
     if (ballot(full && near > a.K)) {
       const int at = lane - l + a.K - 1;
@@ -555,7 +625,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       int other = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (i >= have || !(key[i] > kNegInf) || last - key[i] > margin) continue;
+        if (!(key[i] >= from)) continue;
         other += clean_logit(mine[i]) == xk && (!a.bias || a.bias[e0 + i] == bk) ? 0 : 1;
       }
       other = lanes_sum<LPR>(other);
