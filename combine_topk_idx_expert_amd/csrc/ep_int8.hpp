@@ -21,12 +21,98 @@ struct QuantArgs {
 // to x / scale, ties to even, of the exact quotient.  A row of zeros has scale
 // 0 and codes 0; a row holding NaN or an infinity has scale NaN and codes 0, so
 // that what is made of it is NaN and seen.
+//
+// m: the largest magnitude's bits (magnitudes order like unsigned integers, NaN
+// and infinities above the rest).
+__device__ __forceinline__ float int8_scale(uint32_t m) {
+  return m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.0f;
+}
+
+// The code by a 64-bit quotient, for rows of any scale.
 __device__ __forceinline__ int8_t int8_code(float x, float scale) {
   if (!(scale > 0.0f)) return 0;
   const double q = rint((double)x / (double)scale);
   return (int8_t)(int)fmin(fmax(q, -127.0), 127.0);
 }
 
+// The code of x by a product with inv = 1 / scale, as its low byte: adding
+// 1.5 * 2^23 rounds to a whole number (to even) and leaves it in the low bits.
+// The rest d = x - r * scale is exact where |d| is near scale / 2 (a multiple of
+// half a step of scale, below 2^24 of them), so |d| < scale / 2 says that r is
+// the nearest code; `off` gathers the largest |d|.
+__device__ __forceinline__ uint32_t int8_code_fast(float x, float scale, float inv, float& off) {
+  const float t = x * inv + 12582912.0f;
+  const float r = t - 12582912.0f;
+  off = fmaxf(off, fabsf(__builtin_fmaf(-r, scale, x)));
+  return __float_as_uint(t);
+}
+
+// Rows held in registers, WAVES waves a row: a lane has NC chunks of 16 bytes,
+// so every byte is read once.  Memory bounds it.  Many rows take a wave each (no
+// barrier); few rows four waves, for the latency.  A chunk in which a quotient
+// lies on or within rounding of a border between two codes is done over in 64
+// bits (one in some thousand).
+template <typename IO, int WAVES, int NC>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
+  constexpr int V = 16 / sizeof(typename IO::type);
+  constexpr int kRows = 4 / WAVES;
+  __shared__ uint32_t part[4];
+  const int lane = lane_id();
+  const int wave = threadIdx.x / kWave;
+  const int64_t row = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? wave : 0);
+  if (row >= a.N) return;
+  const int chunks = a.H / V;
+  const int c0 = (WAVES == 1 ? 0 : wave * kWave) + lane;
+  const u32x4* src = (const u32x4*)((const typename IO::type*)a.x + row * a.stride);
+  u32x4 raw[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = c0 + i * WAVES * kWave;
+    raw[i] = u32x4{0, 0, 0, 0};
+    if (c < chunks) raw[i] = __builtin_nontemporal_load(src + c);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) m = IO::max_magnitude(m, raw[i]);
+  m = IO::magnitude_bits(m);
+  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+  if (WAVES > 1) {
+    if (lane == 0) part[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) m = max(m, part[w]);
+  }
+  const float scale = int8_scale(m);
+  if (threadIdx.x % (WAVES * kWave) == 0) a.scales[row] = scale;
+  const bool plain = scale > 0x1p-100f;  // neither 1 / scale nor the rests leave the normal range
+  const float inv = 1.0f / scale, half = 0.5f * scale;
+  typedef uint32_t out_t __attribute__((ext_vector_type(V / 4)));
+  out_t* dst = (out_t*)(a.codes + row * a.H);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = c0 + i * WAVES * kWave;
+    float f[V];
+    IO::unpack(raw[i], f);
+    uint32_t b[V];
+    float off = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = int8_code_fast(f[j], scale, inv, off);
+    if (!plain || off >= half) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) b[j] = (uint8_t)int8_code(f[j], scale);
+    }
+    out_t o;
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      const uint32_t lo = __builtin_amdgcn_perm(b[4 * j + 1], b[4 * j], 0x0C0C0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(b[4 * j + 3], b[4 * j + 2], 0x0C0C0400u);
+      o[j] = lo | hi << 16;
+    }
+    if (c < chunks) __builtin_nontemporal_store(o, dst + c);
+  }
+}
+
+// Any row length, stride and alignment: two passes over the row.
 constexpr int kQuantThreads = 256;
 
 template <typename IO>
@@ -34,7 +120,6 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantArgs a) {
   __shared__ uint32_t part[kQuantThreads / kWave];
   const int64_t row = blockIdx.x;
   const int64_t base = row * a.stride;
-  // magnitudes order like unsigned integers, NaN and infinities above the rest
   uint32_t m = 0;
   for (int i = threadIdx.x; i < a.H; i += kQuantThreads)
     m = max(m, __float_as_uint(IO::load(a.x, base + i)) & 0x7FFFFFFFu);
@@ -42,7 +127,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantArgs a) {
   if (lane_id() == 0) part[threadIdx.x / kWave] = m;
   __syncthreads();
   for (int w = 0; w < kQuantThreads / kWave; ++w) m = max(m, part[w]);
-  const float scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.0f;
+  const float scale = int8_scale(m);
   if (threadIdx.x == 0) a.scales[row] = scale;
   for (int i = threadIdx.x; i < a.H; i += kQuantThreads)
     a.codes[row * a.H + i] = int8_code(IO::load(a.x, base + i), scale);

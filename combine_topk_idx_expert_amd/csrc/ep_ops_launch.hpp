@@ -5,6 +5,8 @@
 // anonymous namespace, after the error helpers (fail, EP_LAUNCHED) it uses.
 #pragma once
 
+constexpr int kCUs = 256;  // MI355X
+
 // Calls f with the element-access type of an EP_TYPE_* value.
 template <typename F>
 ep_status with_type(int32_t type, F f) {
@@ -96,14 +98,32 @@ ep_status launch_route_backward(const RouteBwdArgs& a, hipStream_t s) {
   return EP_OK;
 }
 
+template <typename IO, int WAVES>
+ep_status launch_quantize_rows(const QuantArgs& a, int nc, hipStream_t s) {
+  const int blocks = (int)((a.N * WAVES + 3) / 4);
+  if (nc <= 1)
+    quantize_rows_kernel<IO, WAVES, 1><<<blocks, 256, 0, s>>>(a);
+  else if (nc <= 2)
+    quantize_rows_kernel<IO, WAVES, 2><<<blocks, 256, 0, s>>>(a);
+  else if (nc <= 4)
+    quantize_rows_kernel<IO, WAVES, 4><<<blocks, 256, 0, s>>>(a);
+  else
+    quantize_rows_kernel<IO, WAVES, 8><<<blocks, 256, 0, s>>>(a);
+  EP_LAUNCHED("quantize_rows_kernel");
+  return EP_OK;
+}
+
 template <typename IO>
 ep_status launch_quantize(const QuantArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(typename IO::type);
+  const int chunks = (a.H + V - 1) / V;
+  const bool vec = a.H % V == 0 && a.stride % V == 0 && !misaligned(a.x, 16) && !misaligned(a.codes, V);
+  if (vec && a.N >= 4 * kCUs && chunks <= 8 * kWave) return launch_quantize_rows<IO, 1>(a, (chunks + 63) / 64, s);
+  if (vec && chunks <= 8 * 4 * kWave) return launch_quantize_rows<IO, 4>(a, (chunks + 255) / 256, s);
   quantize_kernel<IO><<<(int)a.N, kQuantThreads, 0, s>>>(a);
   EP_LAUNCHED("quantize_kernel");
   return EP_OK;
 }
-
-constexpr int kCUs = 256;  // MI355X
 
 template <typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
 ep_status launch_matmul_tile(const MatmulArgs& a, hipStream_t s) {

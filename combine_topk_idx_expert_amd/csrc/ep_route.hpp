@@ -41,6 +41,17 @@ struct RouteBwdArgs {
   float scale;
 };
 
+// Pairs of 16-bit magnitudes: their running maxima (v_pk_max_u16), the larger of
+// the two at the end.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_magnitude16(uint32_t m, u32x4 w) {
+  u16x2 r = __builtin_bit_cast(u16x2, m);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r = __builtin_elementwise_max(r, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t larger16(uint32_t m) { return max(m >> 16, m & 0xFFFFu); }
+
 struct F32 {
   typedef float type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
@@ -49,6 +60,13 @@ struct F32 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
   }
+  // running maximum of magnitudes in a word, and at the end its fp32 bits
+  static __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, u32x4 w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return m; }
   // eight values to an address that is a multiple of 16 bytes
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -58,6 +76,8 @@ struct F32 {
 };
 struct Bf16 {
   typedef uint16_t type;
+  static __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, u32x4 w) { return max_magnitude16(m, w); }
+  static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return larger16(m) << 16; }
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
     return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
   }
@@ -78,6 +98,10 @@ struct Bf16 {
 };
 struct F16 {
   typedef uint16_t type;
+  static __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, u32x4 w) { return max_magnitude16(m, w); }
+  static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) {
+    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)larger16(m)));  // (an infinity or NaN stays one)
+  }
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((_Float16*)p)[i] = (_Float16)v; }
   static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
