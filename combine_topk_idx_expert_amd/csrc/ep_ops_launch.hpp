@@ -89,8 +89,24 @@ ep_status launch_route(const RouteArgs& a, hipStream_t s) {
   return EP_OK;
 }
 
+template <typename IO, int LPR>
+ep_status launch_route_backward_lanes(const RouteBwdArgs& a, hipStream_t s) {
+  constexpr int kRows = kWave / LPR, V = 16 / sizeof(typename IO::type);
+  const bool dense = !a.sigmoid && !a.renorm;
+  const int vec = a.E % V == 0 && !misaligned(a.grad, 16) &&
+                  (!dense || (a.stride % V == 0 && !misaligned(a.logits, 16)));
+  const size_t lds = (size_t)kRows * a.E * sizeof(float);
+  const int blocks = (int)std::min<int64_t>((a.T + kRows - 1) / kRows, 16 * kCUs);
+  route_backward_lanes_kernel<IO, LPR><<<blocks, kWave, lds, s>>>(a, vec);
+  EP_LAUNCHED("route_backward_lanes_kernel");
+  return EP_OK;
+}
+
+// Up to 16 choices of 1024 experts: several rows a wave (at most 32 KiB of LDS).
 template <typename IO>
 ep_status launch_route_backward(const RouteBwdArgs& a, hipStream_t s) {
+  if (a.E <= 1024 && a.K <= 8) return launch_route_backward_lanes<IO, 8>(a, s);
+  if (a.E <= 1024 && a.K <= 16) return launch_route_backward_lanes<IO, 16>(a, s);
   const int blocks = (a.T + kRouteWaves - 1) / kRouteWaves;
   const size_t lds = (size_t)kRouteWaves * a.E * sizeof(float);
   route_backward_kernel<IO><<<blocks, kRouteWaves * kWave, lds, s>>>(a);

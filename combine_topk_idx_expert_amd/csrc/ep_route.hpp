@@ -67,6 +67,11 @@ struct F32 {
     return m;
   }
   static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return m; }
+  // 16 bytes of values
+  static __device__ __forceinline__ void store_piece(float* p, const float* v) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)p);
+  }
   // eight values to an address that is a multiple of 16 bytes
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -91,6 +96,10 @@ struct Bf16 {
       f[2 * i + 1] = bf16_hi(w[i]);
     }
   }
+  static __device__ __forceinline__ void store_piece(uint16_t* p, const float* v) {
+    __builtin_nontemporal_store(u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                      pack_bf16x2(v[6], v[7])}, (u32x4*)p);
+  }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     *(u32x4*)((uint16_t*)p + i) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                         pack_bf16x2(v[6], v[7])};
@@ -110,6 +119,11 @@ struct F16 {
       f[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)w[i]);
       f[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] >> 16));
     }
+  }
+  static __device__ __forceinline__ void store_piece(uint16_t* p, const float* v) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    __builtin_nontemporal_store(f16x8{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3], (_Float16)v[4],
+                                      (_Float16)v[5], (_Float16)v[6], (_Float16)v[7]}, (f16x8*)p);
   }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -769,6 +783,158 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
   if (first) buf[at] = (float)(buf[at] + total);
   wave_sync();
   for (int e = lane; e < a.E; e += kWave) IO::store(a.grad, row * a.E + e, buf[e]);
+}
+
+// The same with LPR lanes a row (K <= LPR), kWave / LPR rows a wave, a lane a
+// choice, in 32 bits.  What has to move is the gradient (and, with a softmax
+// that is not renormalised, the logits): the choices' terms are put into rows of
+// zeros in LDS, the rows go out in 16-byte pieces, and the terms are taken out
+// again, so that the zeros are written to LDS once for all rows of a wave.
+template <typename IO, int LPR>
+__global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArgs a, int vec) {
+  constexpr int kRows = kWave / LPR;
+  constexpr int V = 16 / sizeof(typename IO::type);
+  extern __shared__ float terms[];  // [kRows][E]
+  const int lane = threadIdx.x;
+  const int l = lane % LPR;
+  const bool dense = !a.sigmoid && !a.renorm;
+  float* const row_terms = terms + (lane / LPR) * a.E;
+  for (int i = lane; i < kRows * a.E; i += kWave) terms[i] = 0.0f;
+  wave_sync();
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.T; row0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = row0 + lane / LPR;
+    const bool live = row < a.T;
+    const int64_t base = (live ? row : 0) * a.stride;
+    int at = -1;
+    float g = 0.0f;
+    if (live && l < a.K) {
+      const int64_t e = a.idx[row * a.K + l];
+      if (e >= 0 && e < a.E) {
+        at = (int)e;
+        g = a.gw[row * a.K + l];
+      }
+    }
+    const bool have = at >= 0;
+    const float x = have ? clean_logit(IO::load(a.logits, base + at)) : kNegInf;
+    // softmax over the whole row: maximum and sum in one pass
+    float m = kNegInf, sum = 0.0f;
+    if (dense) {
+      auto add = [&](const float* f, int n) {
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < n) top = fmaxf(top, clean_logit(f[i]));
+        const float old = m > kNegInf ? sum * expf(m - top) : sum;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < n && !(f[i] <= kNegInf)) s += expf(clean_logit(f[i]) - top);  // NaN stays NaN
+        sum = old + s;
+        m = top;
+      };
+      if (vec) {
+        const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+        for (int c = l; c < a.E / V; c += LPR) {
+          float f[V];
+          IO::unpack(src[c], f);
+          add(f, V);
+        }
+      } else {
+        for (int e = l; e < a.E; e += LPR) {
+          float f[V] = {IO::load(a.logits, base + e)};
+          add(f, 1);
+        }
+      }
+      const float top = lanes_max<LPR>(m);
+      sum = lanes_sum<LPR>(m > kNegInf ? sum * expf(m - top) : sum);
+      m = top;
+    }
+    float d = 0.0f, inner = 0.0f;
+    if (a.renorm) {
+      const float top = lanes_max<LPR>(x);
+      const float t = fminf(top, 0.0f);
+      float w = 0.0f;
+      if (x > kNegInf)
+        w = !a.sigmoid ? expf(x - top) : x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - t) / (1.0f + expf(x));
+      const float total = lanes_sum<LPR>(w);
+      if (total > 0.0f) w /= total;
+      const float mean = lanes_sum<LPR>(have ? g * w : 0.0f);
+      d = w * (g - mean) * a.scale;
+      if (a.sigmoid) d /= 1.0f + expf(x);
+    } else if (a.sigmoid) {
+      if (x > kNegInf) d = a.scale * g / ((1.0f + expf(-x)) * (1.0f + expf(x)));
+    } else {
+      const float p = x > kNegInf ? expf(x - m) / sum : 0.0f;
+      d = a.scale * g * p;
+      inner = a.scale * lanes_sum<LPR>(have ? g * p : 0.0f);
+    }
+    if (!have) d = 0.0f;
+    // slots that name the same expert: the first of them carries the sum
+    float total = d;
+    bool first = have;
+    auto other = [&](int oat, float od, int ol) {
+      const bool same = oat == at;
+      total += same ? od : 0.0f;
+      first = first && !(same && ol < l);
+    };
+    other(xor_lane<1>(at), xor_lane<1>(d), l ^ 1);
+    other(xor_lane<2>(at), xor_lane<2>(d), l ^ 2);
+    other(xor_lane<3>(at), xor_lane<3>(d), l ^ 3);
+    other(xor_lane<4>(at), xor_lane<4>(d), l ^ 4);
+    other(xor_lane<5>(at), xor_lane<5>(d), l ^ 5);
+    other(xor_lane<6>(at), xor_lane<6>(d), l ^ 6);
+    other(xor_lane<7>(at), xor_lane<7>(d), l ^ 7);
+    if (LPR == 16) {
+      other(xor_lane<8>(at), xor_lane<8>(d), l ^ 8);
+      other(xor_lane<9>(at), xor_lane<9>(d), l ^ 9);
+      other(xor_lane<10>(at), xor_lane<10>(d), l ^ 10);
+      other(xor_lane<11>(at), xor_lane<11>(d), l ^ 11);
+      other(xor_lane<12>(at), xor_lane<12>(d), l ^ 12);
+      other(xor_lane<13>(at), xor_lane<13>(d), l ^ 13);
+      other(xor_lane<14>(at), xor_lane<14>(d), l ^ 14);
+      other(xor_lane<15>(at), xor_lane<15>(d), l ^ 15);
+    }
+    if (first) row_terms[at] = total;
+    wave_sync();
+    if (!dense && vec) {
+      // rows are neighbours in memory: the wave writes them as one piece
+      const int pieces = (int)min((int64_t)kRows, a.T - row0) * (a.E / V);
+      typename IO::type* dst = (typename IO::type*)a.grad + row0 * a.E;
+      for (int c = lane; c < pieces; c += kWave) {
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = terms[c * V + i];
+        IO::store_piece(dst + c * V, f);
+      }
+    } else if (live) {
+      const bool any = inner != 0.0f || (ballot(have) >> (lane - l) & (LPR == 16 ? 0xFFFFull : 0xFFull)) != 0;
+      const float back = dense && any ? -inner / sum : 0.0f;  // (a token without a choice: zeros, whatever its logits)
+      if (vec) {
+        const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+        typename IO::type* dst = (typename IO::type*)a.grad + row * a.E;
+        for (int c = l; c < a.E / V; c += LPR) {
+          float f[V], t[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) t[i] = row_terms[c * V + i];
+          if (any) {
+            IO::unpack(src[c], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[i] += back * expf(clean_logit(f[i]) - m);
+          }
+          IO::store_piece(dst + c * V, t);
+        }
+      } else {
+        for (int e = l; e < a.E; e += LPR) {
+          float t = row_terms[e];
+          if (dense && any) t += back * expf(clean_logit(IO::load(a.logits, base + e)) - m);
+          IO::store(a.grad, row * a.E + e, t);
+        }
+      }
+    }
+    wave_sync();
+    if (first) row_terms[at] = 0.0f;
+    wave_sync();
+  }
 }
 
 }  // namespace ep
