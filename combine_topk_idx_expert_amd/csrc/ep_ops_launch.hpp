@@ -97,7 +97,15 @@ ep_status launch_route_backward_lanes(const RouteBwdArgs& a, hipStream_t s) {
                   (!dense || (a.stride % V == 0 && !misaligned(a.logits, 16)));
   const size_t lds = (size_t)kRows * a.E * sizeof(float);
   const int blocks = (int)std::min<int64_t>((a.T + kRows - 1) / kRows, 16 * kCUs);
-  route_backward_lanes_kernel<IO, LPR><<<blocks, kWave, lds, s>>>(a, vec);
+  const int pieces = (a.E / V + LPR - 1) / LPR;  // of a row, a lane
+  if (dense && vec && pieces <= 2)
+    route_backward_lanes_kernel<IO, LPR, 2><<<blocks, kWave, lds, s>>>(a, vec);
+  else if (dense && vec && pieces <= 4)
+    route_backward_lanes_kernel<IO, LPR, 4><<<blocks, kWave, lds, s>>>(a, vec);
+  else if (dense && vec && pieces <= 8)
+    route_backward_lanes_kernel<IO, LPR, 8><<<blocks, kWave, lds, s>>>(a, vec);
+  else
+    route_backward_lanes_kernel<IO, LPR, 0><<<blocks, kWave, lds, s>>>(a, vec);
   EP_LAUNCHED("route_backward_lanes_kernel");
   return EP_OK;
 }

@@ -790,7 +790,9 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
 // that is not renormalised, the logits): the choices' terms are put into rows of
 // zeros in LDS, the rows go out in 16-byte pieces, and the terms are taken out
 // again, so that the zeros are written to LDS once for all rows of a wave.
-template <typename IO, int LPR>
+// NCH > 0: the dense form with a lane's NCH pieces of the row in registers, read
+// and raised once; 0: every other case.
+template <typename IO, int LPR, int NCH>
 __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArgs a, int vec) {
   constexpr int kRows = kWave / LPR;
   constexpr int V = 16 / sizeof(typename IO::type);
@@ -818,7 +820,32 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
     const float x = have ? clean_logit(IO::load(a.logits, base + at)) : kNegInf;
     // softmax over the whole row: maximum and sum in one pass
     float m = kNegInf, sum = 0.0f;
-    if (dense) {
+    float e[NCH > 0 ? NCH : 1][V];
+    if (NCH > 0) {
+      const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = j * LPR + l;
+        const bool in = c < a.E / V;
+        IO::unpack(src[in ? c : 0], e[j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          nan |= in && e[j][i] != e[j][i];
+          e[j][i] = in ? clean_logit(e[j][i]) : kNegInf;
+          m = fmaxf(m, e[j][i]);
+        }
+      }
+      m = fmaxf(lanes_max<LPR>(m), -3.402823466e38f);  // finite, also in a row of -Inf
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          e[j][i] = fast_exp(e[j][i] - m);
+          sum += e[j][i];
+        }
+      sum = lanes_sum<LPR>(nan ? __uint_as_float(0x7FC00000u) : sum);
+    } else if (dense) {
       auto add = [&](const float* f, int n) {
         float top = m;
 #pragma unroll
@@ -896,7 +923,7 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
     }
     if (first) row_terms[at] = total;
     wave_sync();
-    if (!dense && vec) {
+    if (NCH == 0 && !dense && vec) {
       // rows are neighbours in memory: the wave writes them as one piece
       const int pieces = (int)min((int64_t)kRows, a.T - row0) * (a.E / V);
       typename IO::type* dst = (typename IO::type*)a.grad + row0 * a.E;
@@ -909,7 +936,18 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
     } else if (live) {
       const bool any = inner != 0.0f || (ballot(have) >> (lane - l) & (LPR == 16 ? 0xFFFFull : 0xFFull)) != 0;
       const float back = dense && any ? -inner / sum : 0.0f;  // (a token without a choice: zeros, whatever its logits)
-      if (vec) {
+      if (NCH > 0) {
+        typename IO::type* dst = (typename IO::type*)a.grad + row * a.E;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+          const int c = j * LPR + l;
+          if (c >= a.E / V) break;
+          float t[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) t[i] = row_terms[c * V + i] + (any ? back * e[j][i] : 0.0f);
+          IO::store_piece(dst + c * V, t);
+        }
+      } else if (vec) {
         const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
         typename IO::type* dst = (typename IO::type*)a.grad + row * a.E;
         for (int c = l; c < a.E / V; c += LPR) {
