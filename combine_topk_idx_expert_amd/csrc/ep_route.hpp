@@ -394,10 +394,11 @@ __device__ __forceinline__ void merge8_lane(double (&v)[8]) {
   merge8(v, o);
 }
 
-// by_sign: -1, or 0 for ~e whatever the key
-__device__ __forceinline__ double tagged(float k, int e, int by_sign) {
+// BY_SIGN: inverted for positive keys only, else always.
+template <bool BY_SIGN>
+__device__ __forceinline__ double tagged(float k, int e) {
   const uint32_t hi = __float_as_uint(k);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | (uint32_t)(~e ^ (((int)hi >> 31) & by_sign)));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | (uint32_t)(~e ^ (BY_SIGN ? (int)hi >> 31 : 0)));
 }
 __device__ __forceinline__ float key_of(double d) {
   return __uint_as_float((uint32_t)(__builtin_bit_cast(uint64_t, d) >> 32));
@@ -405,6 +406,24 @@ __device__ __forceinline__ float key_of(double d) {
 __device__ __forceinline__ int expert_of(double d, int by_sign) {
   const uint64_t b = __builtin_bit_cast(uint64_t, d);
   return ~((int)(uint32_t)b ^ (((int)(uint32_t)(b >> 32) >> 31) & by_sign));
+}
+
+// The best eight of a lane's keys, falling.
+template <int VPL, bool BY_SIGN>
+__device__ __forceinline__ void best_of_lane(const float (&key)[VPL], int e0, double (&list)[8]) {
+#pragma unroll
+  for (int c = 0; c < VPL; c += 8) {
+    double v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = tagged<BY_SIGN>(key[c + i], e0 + c + i);
+    sort8(v);
+    if (c == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) list[i] = v[i];
+    } else {
+      merge8(list, v);
+    }
+  }
 }
 
 struct RouteLanes {
@@ -419,6 +438,15 @@ struct RouteLanes {
 // log2(e) * x for exp2, and the hardware's exp2 and reciprocal: the scores of
 // the first pass, whose errors the margins below bound.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// A choice's score relative to the largest of the token's: softmax exp(x - best),
+// sigmoid exp(x - t) / (1 + exp(x)), t = min(best, 0).
+__device__ __forceinline__ float choice_weight(float x, float best, int sigmoid) {
+  if (!sigmoid) return expf(x - best);
+  const float a = expf(-fabsf(x));
+  const float top = x > 0.0f ? 1.0f : best < 0.0f ? expf(x - best) : a;
+  return top / (1.0f + a);
+}
 
 template <typename IO, int LPR, int VPL>
 __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLanes p) {
@@ -475,7 +503,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   const int e0 = l * p.seg;
   const int have = max(0, min(p.seg, a.E - e0));
   float key[VPL];
-  float top = kNegInf, bottom = __builtin_inff();
+  float top = kNegInf;
 #pragma unroll
   for (int i = 0; i < VPL; i += 4) {
     f32x4 v = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -483,28 +511,27 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
 #pragma unroll
     for (int j = 0; j < 4; ++j) key[i + j] = v[j];
   }
+  float size = 0.0f;  // NaN if one of them is
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    top = __builtin_elementwise_maximum(top, key[i]);  // NaN if one of them is
-    bottom = __builtin_elementwise_minimum(bottom, key[i]);
-  }
-  const bool special = ballot(have < VPL || !(top < __builtin_inff()) || !(bottom > kNegInf)) != 0;
+  for (int i = 0; i < VPL; i += 2)
+    size = __builtin_elementwise_maximum(__builtin_elementwise_maximum(size, fabsf(key[i])), fabsf(key[i + 1]));
+  const bool special = ballot(have < VPL || !(size < __builtin_inff())) != 0;
   bool any_nan = false;
   if (special) {
     bool nan = false;
-    top = kNegInf;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const float x = i < have ? key[i] : kNegInf;
       nan |= x != x;
       key[i] = x != x ? kNegInf : clean_logit(x);
-      top = fmaxf(top, key[i]);
     }
     const uint64_t row_lanes = (LPR == 16 ? 0xFFFFull : 0xFFull) << (lane - l);
     any_nan = (ballot(nan) & row_lanes) != 0;
   }
   float total = 1.0f;
   if (!a.sigmoid && (!by_logit || !a.renorm)) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) top = fmaxf(top, key[i]);
     top = fmaxf(lanes_max<LPR>(top), -3.402823466e38f);  // finite, also in a row without a choice
     float sum = 0.0f;
 #pragma unroll
@@ -541,7 +568,8 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
         for (int i = 0; i < VPL; ++i) key[i] += a.bias[i < have ? e0 + i : 0];
       }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) best = __builtin_elementwise_maximum(best, key[i]);
+      for (int i = 0; i < VPL; i += 2)
+        best = __builtin_elementwise_maximum(__builtin_elementwise_maximum(best, key[i]), key[i + 1]);
       // a key of -Inf or NaN cannot be chosen; one of +Inf is decided in 64 bits
       if (ballot(!(best < __builtin_inff()))) {
 #pragma unroll
@@ -554,13 +582,13 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   // 2^-22; softmax: the sum's error too, below 2^-18 of the largest score) and
   // of the sum with the bias
   const float margin0 = a.sigmoid ? 0x1p-20f : 0x1p-16f * __builtin_amdgcn_rcpf(total);
-  bool unsure = false;
+  bool unsure = false, lane_kept = true;
 
   if (a.G > 1) {
     float m1 = kNegInf, m2 = kNegInf;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      m2 = fmaxf(m2, fminf(m1, key[i]));
+      m2 = __builtin_amdgcn_fmed3f(m1, m2, key[i]);  // m1 >= m2: the second of the three
       m1 = fmaxf(m1, key[i]);
     }
     auto join = [&](float o1, float o2) {
@@ -604,25 +632,18 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       const float margin = (a.top2 ? 2.0f : 1.0f) * margin0 + 0x1p-21f * fmaxf(fabsf(worst), fabsf(best));
       unsure |= best > kNegInf && !(worst - best > margin);
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = kept ? key[i] : kNegInf;
+    lane_kept = kept;
   }
 
-  const int by_sign = by_logit ? -1 : 0;
   double list[8];
+  if (by_logit)
+    best_of_lane<VPL, true>(key, e0, list);
+  else
+    best_of_lane<VPL, false>(key, e0, list);
+  const double none = tagged<true>(kNegInf, 0);
+  double own[8];
 #pragma unroll
-  for (int c = 0; c < VPL; c += 8) {
-    double v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = tagged(key[c + i], e0 + c + i, by_sign);
-    sort8(v);
-    if (c == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) list[i] = v[i];
-    } else {
-      merge8(list, v);
-    }
-  }
+  for (int i = 0; i < 8; ++i) own[i] = list[i] = lane_kept ? list[i] : none;
   merge8_lane<1>(list);
   merge8_lane<2>(list);
   merge8_lane<7>(list);
@@ -633,7 +654,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
 #pragma unroll
   for (int i = 1; i < 8; ++i) mine_d = l == i ? list[i] : mine_d;
   const bool chosen = l < a.K && key_of(mine_d) > kNegInf;
-  const int e = chosen ? expert_of(mine_d, by_sign) : 0;
+  const int e = chosen ? expert_of(mine_d, by_logit ? -1 : 0) : 0;
   const int o = (e * p.magic) >> 20;
   const float x = chosen ? clean_logit(row_lds[o * p.pitch + (e - o * p.seg)]) : kNegInf;
 
@@ -653,17 +674,20 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     const float last = key_of(last_d);
     const bool full = last > kNegInf;
     const float from = last - margin;
-    int near = 0;
+    // the best key left out: a lane's choices are the first of its eight; eight
+    // of one lane leave its ninth unknown
+    float out = key_of(own[7]);
+    out = own[7] < last_d ? out : __builtin_inff();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) near += key[i] >= from ? 1 : 0;
-    near = lanes_sum<LPR>(near);
-    if (ballot(full && near > a.K)) {
+    for (int i = 6; i >= 0; --i) out = own[i] < last_d ? key_of(own[i]) : out;
+    out = lanes_max<LPR>(lane_kept ? out : kNegInf);
+    if (ballot(full && out >= from)) {
       const int at = lane - l + a.K - 1;
       const float xk = __shfl(x, at, 64), bk = __shfl(b, at, 64);
       int other = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (!(key[i] >= from)) continue;
+        if (!(lane_kept && key[i] >= from)) continue;
         other += clean_logit(mine[i]) == xk && (!a.bias || a.bias[e0 + i] == bk) ? 0 : 1;
       }
       other = lanes_sum<LPR>(other);
@@ -676,14 +700,11 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   float w = 0.0f;
   if (a.renorm) {
     const float best = lanes_max<LPR>(x);
-    if (chosen) {
-      const float t = fminf(best, 0.0f);
-      w = !a.sigmoid ? expf(x - best) : x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - t) / (1.0f + expf(x));
-    }
+    if (chosen) w = choice_weight(x, best, a.sigmoid);
     const float sum = lanes_sum<LPR>(w);
     if (chosen) w /= sum;
   } else if (chosen) {
-    w = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - top) / total;
+    w = a.sigmoid ? choice_weight(x, 0.0f, 1) : expf(x - top) / total;
   }
   if (l < a.K && row0 + lane / LPR < a.T) {
     const bool put = chosen && (!a.mask || a.mask[row] != 0);
