@@ -306,11 +306,11 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // Value of lane (lane ^ X), X < 16, by DPP.
 template <int X>
 __device__ __forceinline__ int xor_lane(int v) {
-  if constexpr (X >= 8) return xor_lane<15 ^ X>(__builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, false));  // mirror of 16
-  else if constexpr (X >= 4) return xor_lane<7 ^ X>(__builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false));  // mirror of 8
-  else if constexpr (X == 3) return __builtin_amdgcn_update_dpp(0, v, 0x1B, 0xF, 0xF, false);
-  else if constexpr (X == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false);
-  else if constexpr (X == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
+  if constexpr (X >= 8) return xor_lane<15 ^ X>(__builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));  // mirror of 16
+  else if constexpr (X >= 4) return xor_lane<7 ^ X>(__builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));  // mirror of 8
+  else if constexpr (X == 3) return __builtin_amdgcn_mov_dpp(v, 0x1B, 0xF, 0xF, true);
+  else if constexpr (X == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (X == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
   else return v;
 }
 template <int X>
