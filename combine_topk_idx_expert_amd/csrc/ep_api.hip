@@ -735,7 +735,7 @@ ep_status ep_quantize_int8(int32_t type, const void* x, int64_t num_rows, int32_
   if (num_rows < 0 || num_cols < 1) return fail(EP_ERR_SHAPE, "bad sizes: %lld rows of %d", (long long)num_rows, num_cols);
   if (num_rows == 0) return EP_OK;
   if (row_stride < num_cols) return fail(EP_ERR_SHAPE, "row_stride %lld below num_cols %d", (long long)row_stride, num_cols);
-  if (num_rows >= ((int64_t)1 << 31) / kQuantThreads || num_cols > EP_MAX_QUANT_COLS || row_stride > ((int64_t)1 << 40))
+  if (num_rows > EP_MAX_QUANT_ROWS || num_cols > EP_MAX_QUANT_COLS || row_stride > ((int64_t)1 << 40))
     return fail(EP_ERR_OVERFLOW, "%lld rows of %d (stride %lld): too large", (long long)num_rows, num_cols,
                 (long long)row_stride);
   if (!x || !codes || !scales) return fail(EP_ERR_NULL, "x / codes / scales is NULL");

@@ -64,13 +64,16 @@ __device__ __forceinline__ void step_sync() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Starts of the groups' row tiles: pre[g] tiles come before group g, pre[G] in all.
+// Starts of the groups' row tiles: pre[g] tiles come before group g, pre[G] in
+// all.  Groups do not overlap, so there are at most M / BM + G tiles; ranges that
+// say otherwise are cut there, which keeps every index in range.
 template <int THREADS, int BM>
 __device__ void tile_starts(const MatmulArgs& a, int* pre) {
+  const int most = (int)(a.M / BM) + a.G;
   for (int g = threadIdx.x; g < a.G; g += THREADS) {
     int64_t lo, hi;
     group_rows(a, g, lo, hi);
-    pre[g] = (int)((hi - lo + BM - 1) / BM);
+    pre[g] = (int)((hi - lo + BM - 1) / BM);  // below 2^24
   }
   __syncthreads();
   if (threadIdx.x < kWave) {
@@ -83,8 +86,8 @@ __device__ void tile_starts(const MatmulArgs& a, int* pre) {
         const int y = __shfl_up(x, o, 64);
         if ((int)threadIdx.x >= o) x += y;
       }
-      if (g < a.G) pre[g] = carry + x - v;
-      carry += __shfl(x, kWave - 1, 64);
+      if (g < a.G) pre[g] = min(carry + x - v, most);
+      carry = min(carry + __shfl(x, kWave - 1, 64), most);
     }
     if (threadIdx.x == 0) pre[a.G] = carry;
   }

@@ -44,8 +44,8 @@ ep_status validate_route(const ep_route_config* c, int32_t type, int64_t num_tok
   if (num_tokens < 0) return fail(EP_ERR_SHAPE, "num_tokens %lld < 0", (long long)num_tokens);
   if (num_tokens > 0 && row_stride < c->num_experts)
     return fail(EP_ERR_SHAPE, "row_stride %lld below num_experts %d", (long long)row_stride, c->num_experts);
-  if (num_tokens * c->num_topk >= ((int64_t)1 << 31) || num_tokens >= ((int64_t)1 << 31))
-    return fail(EP_ERR_OVERFLOW, "num_tokens * num_topk reaches 2^31");
+  if (num_tokens > EP_MAX_ROUTE_TOKENS)
+    return fail(EP_ERR_OVERFLOW, "num_tokens %lld above %d", (long long)num_tokens, EP_MAX_ROUTE_TOKENS);
   if (row_stride > ((int64_t)1 << 40)) return fail(EP_ERR_OVERFLOW, "row_stride %lld too large", (long long)row_stride);
   return EP_OK;
 }
@@ -166,9 +166,12 @@ template <typename IO, bool GATED, int MT, int NT, int KW, int S>
 ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
   const int bc = (GATED ? NT / 2 : NT) * 16;
   const int64_t nb = (a.width + bc - 1) / bc;
-  const int64_t rows = a.row_start ? std::min(a.M, a.most) : a.M;
-  const int y = (int)std::min<int64_t>((rows + 16 * MT - 1) / (16 * MT), 4096);
-  matmul_split_kernel<IO, GATED, MT, NT, KW, S><<<dim3((unsigned)nb, y, a.G), KW * kWave, 0, s>>>(a);
+  // row tiles side by side; a workgroup takes several where there are more.  For
+  // groups: twice the mean, or what fills the card
+  int64_t y = std::min<int64_t>((std::min(a.M, a.most) + 16 * MT - 1) / (16 * MT), 4096);
+  if (a.row_start)
+    y = std::min(y, std::max<int64_t>((2 * a.M / a.G + 16 * MT - 1) / (16 * MT), 32 * kCUs / (nb * a.G) + 1));
+  matmul_split_kernel<IO, GATED, MT, NT, KW, S><<<dim3((unsigned)nb, (unsigned)y, a.G), KW * kWave, 0, s>>>(a);
   EP_LAUNCHED("matmul_split_kernel");
   return EP_OK;
 }

@@ -70,6 +70,8 @@ extern "C" {
 #define EP_MAX_EXPERTS 4096
 #define EP_MAX_TOPK 32
 #define EP_MAX_ROUTE_GROUPS 64
+#define EP_MAX_ROUTE_TOKENS (1 << 25)
+#define EP_MAX_QUANT_ROWS (1 << 23)
 #define EP_MAX_QUANT_COLS (1 << 24)
 #define EP_MAX_MATMUL_INNER 131056 /* 128 * 128 * inner stays below 2^31 */
 #define EP_MAX_MATMUL_OUTER (1 << 20)

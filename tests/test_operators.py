@@ -438,6 +438,14 @@ def test_product_many_groups():
         starts = (np.cumsum(counts) - counts).tolist()
         say("product groups", G)
         check_product(g, max(sum(counts), 1), 64, 48, counts, starts, True, torch.float32)
+    # among them large ones, at the ends and in between, so that both kernels have their share
+    for G, K, N in ((4096, 64, 64), (1000, 144, 48), (65, 256, 516), (64, 80, 512)):
+        counts = r.integers(0, 3, G)
+        counts[r.choice(G, min(G, 150), replace=False)] = r.integers(60, 300, min(G, 150))
+        counts[0], counts[-1] = 300, 77
+        starts = np.cumsum(counts) - counts
+        say("product groups, some large", G)
+        check_product(g, int(counts.sum()) + 3, K, N, counts.tolist(), starts.tolist(), G % 2 == 0, torch.float32)
 
 
 def test_product_group_order_and_ranges_outside_the_rows():

@@ -63,7 +63,7 @@ def test_route_arguments_are_checked(L):
         assert call(L, type=3) == S.ERR_SHAPE
         assert call(L, T=-1) == S.ERR_SHAPE
         assert call(L, stride=255) == S.ERR_SHAPE
-        assert call(L, T=1 << 28) == S.ERR_OVERFLOW
+        assert call(L, T=(1 << 25) + 1) == S.ERR_OVERFLOW
         assert call(L, stride=1 << 41) == S.ERR_OVERFLOW
         assert call(L, logits=None) == S.ERR_NULL
         assert call(L, logits=2) == S.ERR_SHAPE
@@ -85,7 +85,7 @@ def test_quantize_arguments_are_checked(L):
     assert quantize(L, rows=-1) == S.ERR_SHAPE
     assert quantize(L, cols=0) == S.ERR_SHAPE
     assert quantize(L, stride=63) == S.ERR_SHAPE
-    assert quantize(L, rows=1 << 31) == S.ERR_OVERFLOW
+    assert quantize(L, rows=(1 << 23) + 1) == S.ERR_OVERFLOW
     assert quantize(L, cols=(1 << 24) + 1, stride=1 << 25) == S.ERR_OVERFLOW
     assert quantize(L, x=None) == S.ERR_NULL and quantize(L, codes=None) == S.ERR_NULL
     assert quantize(L, scales=None) == S.ERR_NULL
