@@ -55,6 +55,8 @@ __device__ __forceinline__ uint32_t larger16(uint32_t m) { return max(m >> 16, m
 struct F32 {
   typedef float type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
+  // one element that no neighbour is read with
+  static __device__ __forceinline__ float load_nt(const void* p, int64_t i) { return __builtin_nontemporal_load((const float*)p + i); }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((float*)p)[i] = v; }
   static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
 #pragma unroll
@@ -86,6 +88,9 @@ struct Bf16 {
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
     return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
   }
+  static __device__ __forceinline__ float load_nt(const void* p, int64_t i) {
+    return __uint_as_float((uint32_t)__builtin_nontemporal_load((const uint16_t*)p + i) << 16);
+  }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
     ((uint16_t*)p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
   }
@@ -112,6 +117,9 @@ struct F16 {
     return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)larger16(m)));  // (an infinity or NaN stays one)
   }
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
+  static __device__ __forceinline__ float load_nt(const void* p, int64_t i) {
+    return (float)__builtin_bit_cast(_Float16, __builtin_nontemporal_load((const uint16_t*)p + i));
+  }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((_Float16*)p)[i] = (_Float16)v; }
   static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
 #pragma unroll
@@ -838,7 +846,7 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
       }
     }
     const bool have = at >= 0;
-    const float x = have ? clean_logit(IO::load(a.logits, base + at)) : kNegInf;
+    const float x = have ? clean_logit(IO::load_nt(a.logits, base + at)) : kNegInf;
     // softmax over the whole row: maximum and sum in one pass
     float m = kNegInf, sum = 0.0f;
     float e[NCH > 0 ? NCH : 1][V];
