@@ -611,17 +611,20 @@ _types: dict = {}
 
 def _type(t, name):
     """EP_TYPE_* of a tensor's dtype."""
-    import torch
+    code = _types.get(t)
+    if code is None:
+        import torch
 
-    if not _types:
         _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    if t not in _types:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t}")
-    return _types[t]
+        if t not in _types:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t}")
+        code = _types[t]
+    return code
 
 
 def _require_rows(t, name, cols=None):
-    """A floating device matrix whose rows may be apart; returns (EP_TYPE_*, row stride)."""
+    """A floating device matrix whose rows may be apart; returns (EP_TYPE_*, rows, columns,
+    row stride, device)."""
     import torch
 
     if not isinstance(t, torch.Tensor):
@@ -629,11 +632,29 @@ def _require_rows(t, name, cols=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     code = _type(t.dtype, name)
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must have shape [rows, {'columns' if cols is None else cols}], got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{name} must have shape [rows, {'columns' if cols is None else cols}], got {tuple(shape)}")
+    n, width = shape
+    if t.is_contiguous():
+        return code, n, width, width, t.device
+    apart, step = t.stride()
+    if width > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return code, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return code, n, width, (apart if n > 1 else width), t.device
+
+
+def _launch(device, fn, *args):
+    """fn(*args, torch's current stream) with ``device`` current.  Calls on a few tokens last
+    as long as their host side, so this keeps to what is needed (a context and its exit are
+    0.5 us)."""
+    import torch
+
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)))
 
 
 def route(rc: RouteConfig, logits, bias=None, token_mask=None, out=None):
@@ -645,22 +666,21 @@ def route(rc: RouteConfig, logits, bias=None, token_mask=None, out=None):
     leaves a token unrouted (ids -1, weights 0); out: optional (topk_idx, topk_weights)."""
     import torch
 
-    code, stride = _require_rows(logits, "logits", rc.E)
-    T, device = logits.shape[0], logits.device
+    E, K = rc.E, rc.K
+    code, T, _, stride, device = _require_rows(logits, "logits", E)
     if bias is not None:
-        _require(bias, torch.float32, (rc.E,), "bias", device)
+        _require(bias, torch.float32, (E,), "bias", device)
     if token_mask is not None:
         _require(token_mask, torch.bool, (T,), "token_mask", device)
     if out is None:
-        idx = torch.empty((T, rc.K), dtype=torch.int64, device=device)
-        w = torch.empty((T, rc.K), dtype=torch.float32, device=device)
+        idx = torch.empty_strided((T, K), (K, 1), dtype=torch.int64, device=device)  # (0.3 us below empty)
+        w = torch.empty_strided((T, K), (K, 1), dtype=torch.float32, device=device)
     else:
         idx, w = out
-        _require(idx, torch.int64, (T, rc.K), "topk_idx", device)
-        _require(w, torch.float32, (T, rc.K), "topk_weights", device)
-    with _on(device):
-        _check(lib().ep_route(ctypes.byref(rc._struct), code, _ptr(logits), T, stride, _ptr(bias), _ptr(token_mask),
-                              _ptr(idx), _ptr(w), _stream(device)))
+        _require(idx, torch.int64, (T, K), "topk_idx", device)
+        _require(w, torch.float32, (T, K), "topk_weights", device)
+    _launch(device, lib().ep_route, ctypes.byref(rc._struct), code, logits.data_ptr(), T, stride, _ptr(bias),
+            _ptr(token_mask), idx.data_ptr(), w.data_ptr())
     return idx, w
 
 
@@ -669,17 +689,15 @@ def route_backward(rc: RouteConfig, logits, topk_idx, grad_weights, out=None):
     [T, E] contiguous in the logits' dtype (out: optional, that tensor)."""
     import torch
 
-    code, stride = _require_rows(logits, "logits", rc.E)
-    T, device = logits.shape[0], logits.device
+    code, T, _, stride, device = _require_rows(logits, "logits", rc.E)
     _require(topk_idx, torch.int64, (T, rc.K), "topk_idx", device)
     _require(grad_weights, torch.float32, (T, rc.K), "grad_weights", device)
     if out is None:
         out = torch.empty((T, rc.E), dtype=logits.dtype, device=device)
     else:
         _require(out, logits.dtype, (T, rc.E), "grad_logits", device)
-    with _on(device):
-        _check(lib().ep_route_backward(ctypes.byref(rc._struct), code, _ptr(logits), T, stride, _ptr(topk_idx),
-                                       _ptr(grad_weights), _ptr(out), _stream(device)))
+    _launch(device, lib().ep_route_backward, ctypes.byref(rc._struct), code, logits.data_ptr(), T, stride,
+            topk_idx.data_ptr(), grad_weights.data_ptr(), out.data_ptr())
     return out
 
 
@@ -689,17 +707,15 @@ def quantize_int8(x, out=None):
     per-channel scales.  out: optional (codes, scales)."""
     import torch
 
-    code, stride = _require_rows(x, "x")
-    N, H = x.shape
+    code, N, H, stride, device = _require_rows(x, "x")
     if out is None:
-        codes = torch.empty((N, H), dtype=torch.int8, device=x.device)
-        scales = torch.empty((N,), dtype=torch.float32, device=x.device)
+        codes = torch.empty_strided((N, H), (H, 1), dtype=torch.int8, device=device)
+        scales = torch.empty_strided((N,), (1,), dtype=torch.float32, device=device)
     else:
         codes, scales = out
-        _require(codes, torch.int8, (N, H), "codes", x.device)
-        _require(scales, torch.float32, (N,), "scales", x.device)
-    with _on(x.device):
-        _check(lib().ep_quantize_int8(code, _ptr(x), N, H, stride, _ptr(codes), _ptr(scales), _stream(x.device)))
+        _require(codes, torch.int8, (N, H), "codes", device)
+        _require(scales, torch.float32, (N,), "scales", device)
+    _launch(device, lib().ep_quantize_int8, code, x.data_ptr(), N, H, stride, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -716,8 +732,7 @@ def expert_rows(h: Handle, out=None):
         start, count = out
         _require(start, torch.int64, (E,), "row_start", h.device)
         _require(count, torch.int32, (E,), "row_count", h.device)
-    with _on(h.device):
-        _check(lib().ep_expert_rows(h.ptr, _ptr(start), _ptr(count), _stream(h.device)))
+    _launch(h.device, lib().ep_expert_rows, h.ptr, start.data_ptr(), count.data_ptr())
     return start, count
 
 
@@ -760,13 +775,13 @@ def matmul_int8(a, w, rows=None, gated: bool = False, out_dtype=None, out=None):
         raise ValueError(f"a gated product needs an even number of channels, got {N}")
     width = N // 2 if gated else N
     if out is None:
-        out = torch.empty((M, width), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=device)
+        out = torch.empty_strided((M, width), (width, 1), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                                  device=device)
     else:
         _require(out, out.dtype if out_dtype is None else out_dtype, (M, width), "out", device)
     code = _type(out.dtype, "out")
-    with _on(device):
-        _check(lib().ep_matmul_int8(_ptr(x), _ptr(xs), M, _ptr(wc), _ptr(wsc), G, _ptr(start), _ptr(count), K, N,
-                                    _GATED if gated else 0, code, _ptr(out), _stream(device)))
+    _launch(device, lib().ep_matmul_int8, x.data_ptr(), xs.data_ptr(), M, wc.data_ptr(), wsc.data_ptr(), G,
+            _ptr(start), _ptr(count), K, N, _GATED if gated else 0, code, out.data_ptr())
     return out
 
 

@@ -14,8 +14,6 @@
 
 namespace ep {
 
-constexpr int kMaxRouteGroups = 64;  // one lane a group
-
 struct RouteArgs {
   const void* logits;    // [T][stride], E used
   int64_t stride;        // elements between rows
@@ -56,7 +54,9 @@ struct F32 {
   typedef float type;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
   // one element that no neighbour is read with
-  static __device__ __forceinline__ float load_nt(const void* p, int64_t i) { return __builtin_nontemporal_load((const float*)p + i); }
+  static __device__ __forceinline__ float load_nt(const void* p, int64_t i) {
+    return __builtin_nontemporal_load((const float*)p + i);
+  }
   static __device__ __forceinline__ void store(void* p, int64_t i, float v) { ((float*)p)[i] = v; }
   static __device__ __forceinline__ void unpack(u32x4 w, float* f) {
 #pragma unroll
@@ -114,7 +114,7 @@ struct F16 {
   typedef uint16_t type;
   static __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, u32x4 w) { return max_magnitude16(m, w); }
   static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) {
-    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)larger16(m)));  // (an infinity or NaN stays one)
+    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)larger16(m)));  // (infinities and NaN stay)
   }
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
   static __device__ __forceinline__ float load_nt(const void* p, int64_t i) {

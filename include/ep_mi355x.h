@@ -421,7 +421,8 @@ ep_status ep_expert_rows(const ep_handle *h, int64_t *row_start, int32_t *row_co
  * y[r][n] = (sum_k a[r][k] * w[g][n][k]) * a_scale[r] * w_scale[g][n], the sum
  * exact in int32, the scales in fp32, rounded once to out_type.  With
  * EP_MATMUL_GATED out[r][n] = silu(y[r][n]) * y[r][n + outer / 2], also from
- * fp32: neither half is rounded before.  inner is a multiple of 16.
+ * fp32: neither half is rounded before.  inner is a multiple of 16; a, w and out
+ * are 16-byte aligned.
  * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
 #define EP_MATMUL_GATED 1u
 ep_status ep_matmul_int8(const int8_t *a, const float *a_scale, int64_t num_rows, const int8_t *w,

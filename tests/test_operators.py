@@ -674,6 +674,45 @@ def test_steps_on_two_streams_at_once():
         s["h"].free()
 
 
+def test_offsets_beyond_32_bits():
+    """Rows more than 2^32 bytes apart and weights beyond 2^32 bytes: the values of the same
+    rows and channels close together."""
+    far = 2 ** 31 + 8  # elements between rows
+    g = torch.Generator(device=DEV).manual_seed(11)
+    near = torch.randn(3, 256, generator=g, device=DEV).bfloat16()
+    store = torch.empty(2 * far + 256, dtype=torch.bfloat16, device=DEV)
+    apart = store.as_strided((3, 256), (far, 1))
+    apart.copy_(near)
+    for K in (4, 9):  # several rows a wave, a row a wave
+        rc = router(256, K)
+        idx, w = ep.route(rc, near)
+        got = ep.route(rc, apart)
+        assert torch.equal(got[0], idx) and torch.equal(got[1], w)
+        gw = torch.randn(3, K, generator=g, device=DEV)
+        assert torch.equal(ep.route_backward(rc, apart, idx, gw), ep.route_backward(rc, near, idx, gw))
+    for cols in (256, 255):  # read in whole pieces, element by element
+        for got, want in zip(ep.quantize_int8(apart[:, :cols]), ep.quantize_int8(near[:, :cols])):
+            assert torch.equal(got, want)
+    del store, apart
+    G, N, K = 3, 65536, 16384  # 3 GiB of weights
+    weights = torch.empty(G * N * K, dtype=torch.int8, device=DEV).random_(-127, 128, generator=g).view(G, N, K)
+    scales = torch.rand(G, N, generator=g, device=DEV)
+    M = 2 ** 18 + 300  # more than 4 GiB of rows, of which the last ones are multiplied
+    a = torch.zeros(M, K, dtype=torch.int8, device=DEV)
+    a[-300:].random_(-127, 128, generator=g)
+    sa = torch.rand(M, generator=g, device=DEV)
+    for n in (300, 40):  # by tiles; forty rows alone by the split
+        rows = (torch.tensor([0, 0, M - n], device=DEV), torch.tensor([0, 0, n], dtype=torch.int32, device=DEV))
+        out = torch.empty(M, 512, dtype=torch.bfloat16, device=DEV)
+        tail = weights[:, -512:].contiguous()
+        ep.matmul_int8((a, sa), (tail, scales[:, -512:].contiguous()), rows=rows, out=out)
+        want = ep.matmul_int8((a[-n:].contiguous(), sa[-n:].contiguous()), (tail[2], scales[2, -512:].contiguous()))
+        assert torch.equal(out[-n:], want)
+        few = (a[-n:].contiguous(), sa[-n:].contiguous())
+        rows = (torch.zeros(3, dtype=torch.int64, device=DEV), torch.tensor([0, 0, n], dtype=torch.int32, device=DEV))
+        assert torch.equal(ep.matmul_int8(few, (weights, scales), rows=rows)[:, -512:], want)
+
+
 def test_bindings_refuse_wrong_tensors():
     rc = router(16, 2)
     x = torch.zeros(4, 16, device=DEV)
