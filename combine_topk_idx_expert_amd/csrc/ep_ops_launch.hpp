@@ -140,10 +140,10 @@ ep_status launch_quantize_rows(const QuantArgs& a, int nc, hipStream_t s) {
 template <typename IO>
 ep_status launch_quantize(const QuantArgs& a, hipStream_t s) {
   constexpr int V = 16 / sizeof(typename IO::type);
-  const int chunks = (a.H + V - 1) / V;
-  const bool vec = a.H % V == 0 && a.stride % V == 0 && !misaligned(a.x, 16) && !misaligned(a.codes, V);
-  if (vec && a.N >= 4 * kCUs && chunks <= 8 * kWave) return launch_quantize_rows<IO, 1>(a, (chunks + 63) / 64, s);
-  if (vec && chunks <= 8 * 4 * kWave) return launch_quantize_rows<IO, 4>(a, (chunks + 255) / 256, s);
+  const int chunks = a.H / V;
+  const bool whole = a.H % V == 0;
+  if (whole && a.N >= 4 * kCUs && chunks <= 8 * kWave) return launch_quantize_rows<IO, 1>(a, (chunks + 63) / 64, s);
+  if (whole && chunks <= 8 * 4 * kWave) return launch_quantize_rows<IO, 4>(a, (chunks + 255) / 256, s);
   quantize_kernel<IO><<<(int)a.N, kQuantThreads, 0, s>>>(a);
   EP_LAUNCHED("quantize_kernel");
   return EP_OK;

@@ -50,8 +50,14 @@ __device__ __forceinline__ uint32_t max_magnitude16(uint32_t m, u32x4 w) {
 }
 __device__ __forceinline__ uint32_t larger16(uint32_t m) { return max(m >> 16, m & 0xFFFFu); }
 
+// 16 bytes at any address a value may have: the memory unit takes them in one
+// access.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+
 struct F32 {
   typedef float type;
+  typedef u32x4_at4 piece;
   static __device__ __forceinline__ float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
   // one element that no neighbour is read with
   static __device__ __forceinline__ float load_nt(const void* p, int64_t i) {
@@ -74,15 +80,16 @@ struct F32 {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)p);
   }
-  // eight values to an address that is a multiple of 16 bytes
+  // eight values to any address
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
-    *(f32x4*)((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
-    *(f32x4*)((float*)p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    *(u32x4_at4*)((float*)p + i) = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+    *(u32x4_at4*)((float*)p + i + 4) = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
   }
 };
 struct Bf16 {
   typedef uint16_t type;
+  typedef u32x4_at2 piece;
   static __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, u32x4 w) { return max_magnitude16(m, w); }
   static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return larger16(m) << 16; }
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
@@ -106,12 +113,13 @@ struct Bf16 {
                                       pack_bf16x2(v[6], v[7])}, (u32x4*)p);
   }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
-    *(u32x4*)((uint16_t*)p + i) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                        pack_bf16x2(v[6], v[7])};
+    *(u32x4_at2*)((uint16_t*)p + i) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                            pack_bf16x2(v[6], v[7])};
   }
 };
 struct F16 {
   typedef uint16_t type;
+  typedef u32x4_at2 piece;
   static __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, u32x4 w) { return max_magnitude16(m, w); }
   static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) {
     return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)larger16(m)));  // (infinities and NaN stay)
@@ -135,8 +143,9 @@ struct F16 {
   }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-    *(f16x8*)((_Float16*)p + i) = f16x8{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3],
-                                        (_Float16)v[4], (_Float16)v[5], (_Float16)v[6], (_Float16)v[7]};
+    *(u32x4_at2*)((_Float16*)p + i) = __builtin_bit_cast(
+        u32x4, f16x8{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3], (_Float16)v[4], (_Float16)v[5],
+                     (_Float16)v[6], (_Float16)v[7]});
   }
 };
 

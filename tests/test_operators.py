@@ -290,6 +290,21 @@ def test_quantize_matches_plain(dtype, rows, cols):
         assert torch.equal(again[0], codes) and torch.equal(again[1], scales)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 8), (3, 61), (5, 520), (1030, 2048), (2, 16392)])
+def test_quantize_writes_its_rows_alone(dtype, rows, cols):
+    """Codes that start at any byte, in the midst of others."""
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, device=DEV).to(DTYPES[dtype])
+    want = ep.quantize_int8(x)
+    for off in (1, 7):
+        store = torch.full((rows * cols + 32,), 99, dtype=torch.int8, device=DEV)
+        codes = store[off:off + rows * cols].view(rows, cols)
+        got = ep.quantize_int8(x, out=(codes, torch.empty(rows, device=DEV)))
+        assert torch.equal(codes, want[0]) and torch.equal(got[1], want[1])
+        assert (store[:off] == 99).all() and (store[off + rows * cols:] == 99).all()
+
+
 def test_quantize_borders_and_odd_values():
     inf, nan = float("inf"), float("nan")
     for dtype in DTYPES.values():
@@ -455,6 +470,27 @@ def test_product_group_order_and_ranges_outside_the_rows():
         counts = [20, 30, 5, 10, 10, 1 << 30, -4, 7]
         starts = [60, 0, -3, M, M + 5, M - 15, 40, 1 << 40]
         check_product(g, M, 256, 192, counts, starts, False, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_writes_its_rows_alone(dtype, gated):
+    """Widths of every remainder: the same as by a product of more channels, and nothing past the end."""
+    g = torch.Generator(device=DEV).manual_seed(17)
+    K = 64
+    for M, widths in ((5, (1, 7, 9, 31, 45)), (2100, (2055, 2061))):  # split, tiles
+        a = (codes(g, M, K), torch.rand(M, generator=g, device=DEV))
+        for width in widths:
+            full = (width + 15) // 16 * 16
+            halves = 2 if gated else 1
+            w = codes(g, halves, full, K), torch.rand(halves, full, generator=g, device=DEV)
+            narrow = tuple(t[:, :width].contiguous().flatten(0, 1) for t in w)
+            store = torch.full((M * width + 64,), 9.0, dtype=DTYPES[dtype], device=DEV)
+            out = store[:M * width].view(M, width)
+            ep.matmul_int8(a, narrow, gated=gated, out=out)
+            want = ep.matmul_int8(a, tuple(t.flatten(0, 1) for t in w), gated=gated, out_dtype=DTYPES[dtype])
+            assert torch.equal(out, want[:, :width]), (M, width)
+            assert (store[M * width:] == 9.0).all()
 
 
 def test_product_largest_sums():
