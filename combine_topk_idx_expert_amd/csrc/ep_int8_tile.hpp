@@ -307,7 +307,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float y = (float)acc[m][n][i] * s * sw[n][i];
-          if (GATED) y = silu(y) * ((float)acc[m][n + NT / 2][i] * s * sw[n + NT / 2][i]);
+          if (GATED) y = silu<IO>(y) * ((float)acc[m][n + NT / 2][i] * s * sw[n + NT / 2][i]);
           v[n * 4 + i] = y;
         }
       store_row<IO, NO * 4>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, v);
