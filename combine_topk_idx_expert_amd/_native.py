@@ -261,7 +261,7 @@ def _require(t, dtype, shape, name, device=None):
         raise ValueError(f"{name} is on {t.device}, the handle on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -749,26 +749,30 @@ def matmul_int8(a, w, rows=None, gated: bool = False, out_dtype=None, out=None):
 
     if not (isinstance(a, tuple) and len(a) == 2 and isinstance(w, tuple) and len(w) == 2):
         raise TypeError("a and w must be pairs (codes, scales)")
-    (x, xs), (wc, wsc) = a, w
-    for t, name, dims in ((x, "a codes", 2), (wc, "w codes", 3 if rows is not None else 2)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != dims:
-            raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    M, K = x.shape
-    device = x.device
-    _require(x, torch.int8, (M, K), "a codes")
-    _require(xs, torch.float32, (M,), "a scales", device)
-    N = wc.shape[-2]
-    G = wc.shape[0] if rows is not None else 0
+    x, xs = a
+    wc, wsc = w
+    if not (isinstance(x, torch.Tensor) and isinstance(wc, torch.Tensor)):
+        raise TypeError("a and w codes must be torch.Tensors")
+    xshape, shape, device = x.shape, wc.shape, x.device
+    if len(xshape) != 2:
+        raise ValueError(f"a codes must have 2 dimensions, got {tuple(xshape)}")
+    M, K = xshape
     start = count = None
+    G = 0
     if rows is not None:
-        if G == 0:
-            raise ValueError("w holds no group")
+        if len(shape) != 3 or shape[0] == 0:
+            raise ValueError(f"w codes must have shape [groups, outer, inner], got {tuple(shape)}")
+        G = shape[0]
         start, count = rows
         _require(start, torch.int64, (G,), "row_start", device)
         _require(count, torch.int32, (G,), "row_count", device)
-    shape = (G, N, K) if rows is not None else (N, K)
+    elif len(shape) != 2:
+        raise ValueError(f"w codes must have shape [outer, inner], got {tuple(shape)}")
+    if shape[-1] != K:
+        raise ValueError(f"w codes have an inner size of {shape[-1]}, a codes of {K}")
+    N = shape[-2]
+    _require(x, torch.int8, xshape, "a codes")
+    _require(xs, torch.float32, (M,), "a scales", device)
     _require(wc, torch.int8, shape, "w codes", device)
     _require(wsc, torch.float32, shape[:-1], "w scales", device)
     if gated and N % 2:
