@@ -50,37 +50,47 @@ ep_status validate_route(const ep_route_config* c, int32_t type, int64_t num_tok
   return EP_OK;
 }
 
-template <typename IO, int LPR, int VPL>
+template <typename IO, int LPR, int VPL, int R>
 ep_status launch_route_lanes(const RouteArgs& a, RouteLanes p, hipStream_t s) {
-  p.pitch = 4 * ((p.seg + 3) / 4 | 1);
-  p.magic = (1 << 20) / p.seg + 1;
-  constexpr int V = sizeof(typename IO::type) == 4 ? 4 : 8;
-  p.vec = p.seg % V == 0 && a.E % V == 0 && a.stride % V == 0 && !misaligned(a.logits, 16);
-  p.bias_vec = p.seg % 4 == 0 && a.E % 4 == 0 && !misaligned(a.bias, 16);
   constexpr int kRows = kWave / LPR;
-  const size_t lds = std::max((size_t)kWave * p.pitch * sizeof(float), (size_t)a.E * sizeof(double));
-  route_lanes_kernel<IO, LPR, VPL><<<(a.T + kRows - 1) / kRows, kWave, lds, s>>>(a, p);
+  p.pad = p.seg != VPL || p.gs * a.G != p.seg * LPR;
+  const size_t lds = std::max(((size_t)kRows * p.row_pitch + VPL) * sizeof(float), (size_t)a.E * sizeof(double));
+  route_lanes_kernel<IO, LPR, VPL, R><<<(a.T + kRows - 1) / kRows, kWave, lds, s>>>(a, p);
   EP_LAUNCHED("route_lanes_kernel");
   return EP_OK;
 }
 
-// Up to 512 experts and 8 choices: several rows a wave.  Lanes own whole shares
-// of groups (a group is 1, 2, 4 or 8 lanes); routers for which that does not
-// come out, and wider ones, take one row a wave.
+template <typename IO, int LPR, int VPL>
+ep_status launch_route_lanes(const RouteArgs& a, const RouteLanes& p, hipStream_t s) {
+  return a.K <= 8 ? launch_route_lanes<IO, LPR, VPL, 1>(a, p, s) : launch_route_lanes<IO, LPR, VPL, 2>(a, p, s);
+}
+
+// Up to 512 experts and 16 choices: several rows a wave.  A group is 1, 2, 4 or 8
+// lanes of eight, or of sixteen where eight lanes of 32 experts do not hold it;
+// routers for which that does not come out, and wider ones, take one row a wave.
 template <typename IO>
 ep_status launch_route(const RouteArgs& a, hipStream_t s) {
-  if (a.K <= 8 && a.E <= 512) {
-    const int lanes = a.E <= 256 ? 8 : 16, gs = a.E / a.G;
+  for (int lanes = 8; a.K <= 16 && lanes <= 16; lanes *= 2) {
+    if (a.G > lanes) continue;
     RouteLanes p{};
-    for (p.shift = 0; p.shift <= 3; ++p.shift) {
-      const int wide = 1 << p.shift;
-      p.seg = a.G == 1 ? (a.E + lanes - 1) / lanes : gs / wide;
-      if (a.G > 1 && (gs % wide != 0 || a.G * wide > lanes || p.seg > 32)) continue;
-      if (lanes == 16) return launch_route_lanes<IO, 16, 32>(a, p, s);
-      if (p.seg <= 8) return launch_route_lanes<IO, 8, 8>(a, p, s);
-      if (p.seg <= 16) return launch_route_lanes<IO, 8, 16>(a, p, s);
-      return launch_route_lanes<IO, 8, 32>(a, p, s);
+    p.gs = a.E / a.G;
+    while (a.G << (p.shift + 1) <= lanes && (a.G == 1 || p.shift < 3)) ++p.shift;
+    const int wide = 1 << p.shift;
+    p.seg = (p.gs + wide - 1) / wide;
+    if (a.G == 1) p.seg = (p.seg + 3) / 4 * 4;
+    if (p.seg > 32) continue;
+    if (a.G == 1 || (p.gs == wide * p.seg && p.seg % 4 == 0)) {
+      p.pitch = 4 * ((p.seg + 3) / 4 | 1);
+      p.row_pitch = lanes * p.pitch;
+      p.magic = (1 << 20) / p.seg + 1;
+    } else {
+      p.row_pitch = (a.E + 3) / 4 * 4;
     }
+    p.bias_vec = p.seg % 4 == 0 && p.gs % 4 == 0 && !misaligned(a.bias, 16);
+    if (lanes == 16) return launch_route_lanes<IO, 16, 32>(a, p, s);
+    if (p.seg <= 8 && a.K <= 8) return launch_route_lanes<IO, 8, 8, 1>(a, p, s);
+    if (p.seg <= 16) return launch_route_lanes<IO, 8, 16>(a, p, s);
+    return launch_route_lanes<IO, 8, 32>(a, p, s);
   }
   const int waves = a.E > 2048 ? kRouteWaves / 2 : kRouteWaves;  // at most 64 KiB of LDS
   const int blocks = (a.T + waves - 1) / waves;

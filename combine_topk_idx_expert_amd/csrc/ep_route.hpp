@@ -303,8 +303,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 
 // --------------------------------------------------------------------------
 // Several rows a wave: LPR lanes share a row of at most LPR * VPL experts and
-// K <= 8 choices.  Lane l owns experts l * seg .. l * seg + seg - 1, brought to
-// its registers through LDS (memory is read in whole lines).
+// K <= 8 * R choices.  A lane owns `seg` consecutive experts, or what is left of
+// its group, brought to its registers through LDS (memory is read in whole lines).
 //
 // Keys are fp32.  A key's bits are taken as the high word of a double, whose
 // order is that of the floats (all of them finite doubles, -Inf included), with
@@ -313,6 +313,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // experts.  (Scores skip the inversion by sign, two operations a key: a row whose
 // last choice has a negative key is done over.)  A lane sorts eights of its keys, keeps the best eight, and three or
 // four bitonic merges over its neighbours leave the row's best eight in every lane.
+// More than eight choices (R = 2) take a second round over the keys below the eighth
+// (65536 x 256 bf16, top 10: 28 us, against 178 with one row a wave in 64 bits).
 //
 // The definition orders the keys by their exact values.  Logits are exact.
 // Scores are not: a row where two neighbours among the choices, the last choice
@@ -425,14 +427,17 @@ __device__ __forceinline__ int expert_of(double d, int by_sign) {
   return ~((int)(uint32_t)b ^ (((int)(uint32_t)(b >> 32) >> 31) & by_sign));
 }
 
-// The best eight of a lane's keys, falling.
-template <int VPL, bool BY_SIGN>
-__device__ __forceinline__ void best_of_lane(const float (&key)[VPL], int e0, double (&list)[8]) {
+// The best eight of a lane's keys, falling; BELOW: of those that come after `limit`.
+template <int VPL, bool BY_SIGN, bool BELOW>
+__device__ __forceinline__ void best_of_lane(const float (&key)[VPL], int e0, double limit, double (&list)[8]) {
 #pragma unroll
   for (int c = 0; c < VPL; c += 8) {
     double v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = tagged<BY_SIGN>(key[c + i], e0 + c + i);
+    for (int i = 0; i < 8; ++i) {
+      v[i] = tagged<BY_SIGN>(key[c + i], e0 + c + i);
+      if (BELOW) v[i] = v[i] < limit ? v[i] : tagged<true>(kNegInf, 0);
+    }
     sort8(v);
     if (c == 0) {
 #pragma unroll
@@ -443,13 +448,19 @@ __device__ __forceinline__ void best_of_lane(const float (&key)[VPL], int e0, do
   }
 }
 
+// Where a row's logits are in LDS: share l of `seg` experts at l * pitch (pitch a
+// multiple of 4 and odd in 16-byte units: no bank conflicts), where no group ends
+// within four experts that are stored at once; otherwise one after the other (pitch
+// and magic 0).
 struct RouteLanes {
-  int seg;      // experts of a lane
-  int pitch;    // floats between lanes in LDS: a multiple of 4, odd in 16-byte units
-  int magic;    // e / seg == (e * magic) >> 20 for e < 1024
-  int shift;    // 1 << shift lanes of a group
-  int vec;      // rows can be read 16 bytes at a time, each chunk within one lane's experts
-  int bias_vec; // so can the bias
+  int seg;        // experts of a lane, at most VPL
+  int gs;         // experts of a group (without groups: all)
+  int shift;      // 1 << shift lanes of a group
+  int pitch;      // floats between lanes in LDS, 0: experts one after the other
+  int row_pitch;  // floats between rows in LDS, a multiple of 4
+  int magic;      // e / seg == (e * magic) >> 20 for e < 512
+  int pad;        // some lane has fewer than VPL experts
+  int bias_vec;   // the bias can be read 16 bytes at a time
 };
 
 // log2(e) * x for exp2, and the hardware's exp2 and reciprocal: the scores of
@@ -465,74 +476,78 @@ __device__ __forceinline__ float choice_weight(float x, float best, int sigmoid)
   return top / (1.0f + a);
 }
 
-template <typename IO, int LPR, int VPL>
+template <typename IO, int LPR, int VPL, int R>
 __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLanes p) {
   constexpr int kRows = kWave / LPR;
-  extern __shared__ float lanes_lds[];  // [64][pitch]
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  extern __shared__ float lanes_lds[];  // [kRows][row_pitch], and VPL that are read past the end
   const int lane = threadIdx.x;
   const int l = lane % LPR;
   const int64_t row0 = (int64_t)blockIdx.x * kRows;
   const int64_t row = min(row0 + lane / LPR, (int64_t)a.T - 1);
   const int64_t base = row * a.stride;
-  float* const mine = lanes_lds + lane * p.pitch;
-  float* const row_lds = lanes_lds + (lane - l) * p.pitch;
+  float* const row_lds = lanes_lds + (lane / LPR) * p.row_pitch;
+  const int group = l >> p.shift, share = l & ((1 << p.shift) - 1);
+  const int e0 = group * p.gs + share * p.seg;
+  const int have = group < a.G ? max(0, min(p.seg, p.gs - share * p.seg)) : 0;
+  const float* const mine = row_lds + (p.pitch ? l * p.pitch : have > 0 ? e0 : 0);
   const bool by_logit = !a.bias && (a.G == 1 || !a.top2);
 
   // logits to LDS
-  constexpr int V = sizeof(typename IO::type) == 4 ? 4 : 8;
-  if (p.vec) {
-    constexpr int kChunks = (VPL + V - 1) / V;
-    u32x4 raw[kChunks];
-    const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
-    const int chunks = a.E / V;
+  constexpr int V = 16 / sizeof(typename IO::type);
+  constexpr int kChunks = (VPL + V - 1) / V;
+  const typename IO::type* src = (const typename IO::type*)a.logits + base;
+  const int chunks = a.E / V;
+  auto place = [&](int e) {
+    const int o = (e * p.magic) >> 20;
+    return row_lds + o * p.pitch + (e - o * p.seg);
+  };
+  u32x4 raw[kChunks];
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      const int c = j * LPR + l;
-      raw[j] = c < chunks ? src[c] : u32x4{0, 0, 0, 0};
-    }
+  for (int j = 0; j < kChunks; ++j) {
+    const int c = j * LPR + l;
+    raw[j] = c < chunks ? *(const typename IO::piece*)(src + c * V) : u32x4{0, 0, 0, 0};
+  }
+  const int last = chunks * V + l;  // fewer than V <= LPR are left
+  float end = 0.0f;
+  if (a.E % V != 0 && last < a.E) end = IO::load(a.logits, base + last);
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      const int c = j * LPR + l;
-      if (c < chunks) {
-        const int e = c * V, o = (e * p.magic) >> 20;
-        float* dst = row_lds + o * p.pitch + (e - o * p.seg);
-        float f[V];
-        IO::unpack(raw[j], f);
+  for (int j = 0; j < kChunks; ++j) {
+    const int c = j * LPR + l;
+    if (c < chunks) {
+      float f[V];
+      IO::unpack(raw[j], f);
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          typedef float f32x4 __attribute__((ext_vector_type(4)));
-          *(f32x4*)(dst + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
-        }
-      }
-    }
-  } else {
-    for (int e = l; e < a.E; e += LPR) {
-      const int o = (e * p.magic) >> 20;
-      row_lds[o * p.pitch + (e - o * p.seg)] = IO::load(a.logits, base + e);
+      for (int i = 0; i < V; i += 4) *(f32x4*)place(c * V + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
     }
   }
+  if (a.E % V != 0 && last < a.E) *place(last) = end;
   wave_sync();
 
-  // this lane's logits.  Rows of numbers alone, in whole shares, go straight on;
-  // where the wave has an infinity, a NaN or a lane with fewer experts than VPL,
-  // kNegInf marks what cannot be chosen.
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
-  const int e0 = l * p.seg;
-  const int have = max(0, min(p.seg, a.E - e0));
+  // this lane's logits.  Rows of numbers alone go straight on; where the wave has an
+  // infinity or a NaN, kNegInf marks what cannot be chosen.
   float key[VPL];
   float top = kNegInf;
+  if (p.pitch) {
 #pragma unroll
-  for (int i = 0; i < VPL; i += 4) {
-    f32x4 v = {kNegInf, kNegInf, kNegInf, kNegInf};
-    if (i < p.seg) v = *(const f32x4*)(mine + i);  // seg is below the pitch, a multiple of 4
+    for (int i = 0; i < VPL; i += 4) {
+      const f32x4 v = *(const f32x4*)(mine + i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) key[i + j] = v[j];
+      for (int j = 0; j < 4; ++j) key[i + j] = v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = mine[i];
+  }
+  if (p.pad) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = i < have ? key[i] : 0.0f;
   }
   float size = 0.0f;  // NaN if one of them is
 #pragma unroll
   for (int i = 0; i < VPL; i += 2)
     size = __builtin_elementwise_maximum(__builtin_elementwise_maximum(size, fabsf(key[i])), fabsf(key[i + 1]));
-  const bool special = ballot(have < VPL || !(size < __builtin_inff())) != 0;
+  const bool special = ballot(!(size < __builtin_inff())) != 0;
   bool any_nan = false;
   if (special) {
     bool nan = false;
@@ -544,16 +559,19 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     }
     const uint64_t row_lanes = (LPR == 16 ? 0xFFFFull : 0xFFull) << (lane - l);
     any_nan = (ballot(nan) & row_lanes) != 0;
+  } else if (p.pad) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = i < have ? key[i] : kNegInf;
   }
   float total = 1.0f;
   if (!a.sigmoid && (!by_logit || !a.renorm)) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) top = fmaxf(top, key[i]);
     top = fmaxf(lanes_max<LPR>(top), -3.402823466e38f);  // finite, also in a row without a choice
-    float sum = 0.0f;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += fast_exp(key[i] - top);  // 0 for kNegInf
-    total = lanes_sum<LPR>(sum);
+    for (int i = 0; i < VPL; ++i) sum[i % 4] += fast_exp(key[i] - top);  // 0 for kNegInf
+    total = lanes_sum<LPR>((sum[0] + sum[1]) + (sum[2] + sum[3]));
   }
   if (by_logit) {
 #pragma unroll
@@ -570,6 +588,9 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     if (special) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = i < have && mine[i] > kNegInf ? key[i] : kNegInf;
+    } else if (p.pad) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = i < have ? key[i] : kNegInf;
     }
     if (a.bias) {
       float best = kNegInf;
@@ -582,7 +603,17 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] += a.bias[i < have ? e0 + i : 0];
+        for (int i = 0; i < VPL; i += 4) {
+          if (i >= have) continue;
+          if (e0 + i + 4 <= a.E) {  // (a neighbour's bias leaves -Inf, or makes a NaN that is cleared below)
+            const u32x4 b = *(const u32x4_at4*)(a.bias + e0 + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) key[i + j] += __uint_as_float(b[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) key[i + j] += a.bias[min(e0 + i + j, a.E - 1)];
+          }
+        }
       }
 #pragma unroll
       for (int i = 0; i < VPL; i += 2)
@@ -594,11 +625,14 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       }
     }
   }
-  // two keys of the row keep their order where they differ by more: twice the
-  // error of a score (sigmoid: exponent and two hardware operations, below
-  // 2^-22; softmax: the sum's error too, below 2^-18 of the largest score) and
-  // of the sum with the bias
-  const float margin0 = a.sigmoid ? 0x1p-20f : 0x1p-16f * __builtin_amdgcn_rcpf(total);
+  // Two keys of the row keep their order where they differ by more than the error of
+  // their difference.  In units of u = 2^-24, sigmoid: the exponent's 2.3 |x| u
+  // weighs x s (1 - s) < 0.23, exp2 0.5 u, the sum u, the reciprocal 2 u: below 4.1 u
+  // a score.  Softmax, of the largest score: two scores' exponent (0.9 u at most),
+  // exp2 2 u and product u each, and the sum's error, a common factor: 14 additions,
+  // exp2 2 u, the exponents 2.3 ln E u, the reciprocal 2 u: 41 u in all, below 2^-18.
+  // The sum with the bias is added where keys are compared.
+  const float margin0 = a.sigmoid ? 0x1p-20f : 0x1p-18f * __builtin_amdgcn_rcpf(total);
   bool unsure = false, lane_kept = true;
 
   if (a.G > 1) {
@@ -616,7 +650,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     if (p.shift >= 1) join(xor_lane<1>(m1), xor_lane<1>(m2));
     if (p.shift >= 2) join(xor_lane<2>(m1), xor_lane<2>(m2));
     if (p.shift >= 3) join(xor_lane<7>(m1), xor_lane<7>(m2));
-    const int g = l >> p.shift;
+    const int g = group;
     // (groups past the last own nothing: -Inf, behind every other or tied with an empty one)
     const float s = a.top2 && m2 > kNegInf ? m1 + m2 : m1;
     int ahead = 0;
@@ -652,42 +686,76 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     lane_kept = kept;
   }
 
-  double list[8];
-  if (by_logit)
-    best_of_lane<VPL, true>(key, e0, list);
-  else
-    best_of_lane<VPL, false>(key, e0, list);
+  double list[8], own[8];
   const double none = tagged<true>(kNegInf, 0);
-  double own[8];
+  double mine_d[R];  // lane l < 8 of the row holds choices l, l + 8, ..
 #pragma unroll
-  for (int i = 0; i < 8; ++i) own[i] = list[i] = lane_kept ? list[i] : none;
-  merge8_lane<1>(list);
-  merge8_lane<2>(list);
-  merge8_lane<7>(list);
-  if (LPR == 16) merge8_lane<15>(list);
+  for (int c = 0; c < R; ++c) {
+    if (c == 0) {
+      if (by_logit)
+        best_of_lane<VPL, true, false>(key, e0, none, list);
+      else
+        best_of_lane<VPL, false, false>(key, e0, none, list);
+    } else {
+      const double limit = list[7];
+      if (by_logit)
+        best_of_lane<VPL, true, true>(key, e0, limit, list);
+      else
+        best_of_lane<VPL, false, true>(key, e0, limit, list);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] = list[i] = lane_kept ? list[i] : none;
+    merge8_lane<1>(list);
+    merge8_lane<2>(list);
+    merge8_lane<7>(list);
+    if (LPR == 16) merge8_lane<15>(list);
+    mine_d[c] = list[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) mine_d[c] = l == i ? list[i] : mine_d[c];
+  }
 
-  // lane l < 8 of the row holds choice l
-  double mine_d = list[0];
+  bool chosen[R];
+  int e[R];
+  float x[R];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) mine_d = l == i ? list[i] : mine_d;
-  const bool chosen = l < a.K && key_of(mine_d) > kNegInf;
-  const int e = chosen ? expert_of(mine_d, by_logit ? -1 : 0) : 0;
-  const int o = (e * p.magic) >> 20;
-  const float x = chosen ? clean_logit(row_lds[o * p.pitch + (e - o * p.seg)]) : kNegInf;
+  for (int c = 0; c < R; ++c) {
+    chosen[c] = (R == 1 || l < 8) && c * 8 + l < a.K && key_of(mine_d[c]) > kNegInf;
+    e[c] = chosen[c] ? expert_of(mine_d[c], by_logit ? -1 : 0) : 0;
+    x[c] = chosen[c] ? clean_logit(*place(e[c])) : kNegInf;
+  }
 
   if (!by_logit) {
-    unsure |= chosen && key_of(mine_d) < 0.0f;
-    const float kf = chosen ? key_of(mine_d) : 0.0f;
-    const float b = a.bias && chosen ? a.bias[e] : 0.0f;
-    const float margin = margin0 + 0x1p-22f * lanes_max<LPR>(fabsf(kf));
+    float kf[R], b[R], largest = 0.0f;
+#pragma unroll
+    for (int c = 0; c < R; ++c) {
+      unsure |= chosen[c] && key_of(mine_d[c]) < 0.0f;
+      kf[c] = chosen[c] ? key_of(mine_d[c]) : 0.0f;
+      b[c] = a.bias && chosen[c] ? a.bias[e[c]] : 0.0f;
+      largest = fmaxf(largest, fabsf(kf[c]));
+    }
+    const float margin = margin0 + 0x1p-22f * lanes_max<LPR>(largest);
     // neighbours among the choices
-    const float k2 = __shfl_down(kf, 1, 64), x2 = __shfl_down(x, 1, 64), b2 = __shfl_down(b, 1, 64);
-    const bool next = __shfl_down((int)chosen, 1, 64) != 0 && l + 1 < a.K;
-    unsure |= chosen && next && !(kf - k2 > margin) && !(x == x2 && b == b2);
-    // the last choice against those left out
+#pragma unroll
+    for (int c = 0; c < R; ++c) {
+      float k2 = __shfl_down(kf[c], 1, 64), x2 = __shfl_down(x[c], 1, 64), b2 = __shfl_down(b[c], 1, 64);
+      bool next = __shfl_down((int)chosen[c], 1, 64) != 0 && l + 1 < min(8, a.K - c * 8);
+      if (c + 1 < R) {
+        const int first = lane - l;
+        const float k3 = __shfl(kf[c + 1 < R ? c + 1 : c], first, 64), x3 = __shfl(x[c + 1 < R ? c + 1 : c], first, 64);
+        const float b3 = __shfl(b[c + 1 < R ? c + 1 : c], first, 64);
+        const bool n3 = __shfl((int)chosen[c + 1 < R ? c + 1 : c], first, 64) != 0;
+        k2 = l == 7 ? k3 : k2;
+        x2 = l == 7 ? x3 : x2;
+        b2 = l == 7 ? b3 : b2;
+        next = l == 7 ? n3 : next;
+      }
+      unsure |= chosen[c] && next && !(kf[c] - k2 > margin) && !(x[c] == x2 && b[c] == b2);
+    }
+    // the last choice against those left out; it is one of the last round's
+    const int at = a.K - 1 - (R - 1) * 8;
     double last_d = list[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) last_d = a.K - 1 == i ? list[i] : last_d;
+    for (int i = 1; i < 8; ++i) last_d = at == i ? list[i] : last_d;
     const float last = key_of(last_d);
     const bool full = last > kNegInf;
     const float from = last - margin;
@@ -699,34 +767,45 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     for (int i = 6; i >= 0; --i) out = own[i] < last_d ? key_of(own[i]) : out;
     out = lanes_max<LPR>(lane_kept ? out : kNegInf);
     if (ballot(full && out >= from)) {
-      const int at = lane - l + a.K - 1;
-      const float xk = __shfl(x, at, 64), bk = __shfl(b, at, 64);
+      const float xk = __shfl(x[R - 1], lane - l + at, 64), bk = __shfl(b[R - 1], lane - l + at, 64);
       int other = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (!(lane_kept && key[i] >= from)) continue;
+        if (!(full && lane_kept && i < have && key[i] >= from)) continue;
         other += clean_logit(mine[i]) == xk && (!a.bias || a.bias[e0 + i] == bk) ? 0 : 1;
       }
       other = lanes_sum<LPR>(other);
-      const int among = lanes_sum<LPR>(chosen && !(x == xk && b == bk) ? 1 : 0);
-      unsure |= full && other != among;
+      int among = 0;
+#pragma unroll
+      for (int c = 0; c < R; ++c) among += chosen[c] && !(x[c] == xk && b[c] == bk) ? 1 : 0;
+      unsure |= full && other != lanes_sum<LPR>(among);
     }
   }
 
   // weights, as route_row forms them
-  float w = 0.0f;
-  if (a.renorm) {
-    const float best = lanes_max<LPR>(x);
-    if (chosen) w = choice_weight(x, best, a.sigmoid);
-    const float sum = lanes_sum<LPR>(w);
-    if (chosen) w /= sum;
-  } else if (chosen) {
-    w = a.sigmoid ? choice_weight(x, 0.0f, 1) : expf(x - top) / total;
+  float w[R], best = kNegInf, sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < R; ++c) best = fmaxf(best, x[c]);
+  if (a.renorm) best = lanes_max<LPR>(best);
+#pragma unroll
+  for (int c = 0; c < R; ++c) {
+    w[c] = 0.0f;
+    if (chosen[c])
+      w[c] = a.renorm ? choice_weight(x[c], best, a.sigmoid)
+             : a.sigmoid ? choice_weight(x[c], 0.0f, 1)
+                         : expf(x[c] - top) / total;
+    sum += w[c];
   }
-  if (l < a.K && row0 + lane / LPR < a.T) {
-    const bool put = chosen && (!a.mask || a.mask[row] != 0);
-    a.idx[row * a.K + l] = put ? e : -1;
-    a.w[row * a.K + l] = !put ? 0.0f : any_nan ? __uint_as_float(0x7FC00000u) : w * a.scale;
+  if (a.renorm) sum = lanes_sum<LPR>(sum);
+#pragma unroll
+  for (int c = 0; c < R; ++c) {
+    const int k = c * 8 + l;
+    if ((R == 1 || l < 8) && k < a.K && row0 + lane / LPR < a.T) {
+      const bool put = chosen[c] && (!a.mask || a.mask[row] != 0);
+      if (a.renorm && chosen[c]) w[c] /= sum;
+      a.idx[row * a.K + k] = put ? e[c] : -1;
+      a.w[row * a.K + k] = !put ? 0.0f : any_nan ? __uint_as_float(0x7FC00000u) : w[c] * a.scale;
+    }
   }
 
   // the rows whose order fp32 does not settle

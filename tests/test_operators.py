@@ -69,6 +69,23 @@ ROUTERS = [
     (320, 10, 64, 7, "top2"),
     (1000, 32, 1, 1, "max"),
     (4096, 32, 64, 9, "top2"),
+    # more than eight choices, and groups that do not share their experts evenly among lanes
+    (256, 10, 1, 1, "max"),
+    (256, 16, 8, 4, "top2"),
+    (61, 9, 1, 1, "max"),
+    (16, 10, 1, 1, "max"),
+    (512, 12, 8, 4, "top2"),
+    (492, 2, 4, 4, "max"),
+    (488, 10, 8, 5, "top2"),
+    (216, 5, 8, 6, "top2"),
+    (204, 8, 4, 3, "max"),
+    (312, 9, 8, 4, "top2"),
+    (255, 8, 3, 2, "top2"),
+    (54, 11, 6, 3, "top2"),
+    (12, 3, 4, 3, "top2"),
+    (72, 8, 8, 8, "max"),
+    (239, 8, 1, 1, "max"),
+    (137, 6, 1, 1, "max"),
 ]
 
 
@@ -113,16 +130,17 @@ def test_route_matches_plain(E, K, groups, kept, group_score, score):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,kept,group_score", [(1, 1, "max"), (8, 4, "top2"), (8, 3, "max")])
-def test_route_ties_go_to_the_lowest_expert(score, groups, kept, group_score):
+@pytest.mark.parametrize("E,K", [(256, 8), (256, 13), (216, 8), (200, 16)])
+def test_route_ties_go_to_the_lowest_expert(score, groups, kept, group_score, E, K):
     """Logits of few values, a zero bias, signed zeros, equal rows: ties everywhere."""
     g = torch.Generator(device=DEV).manual_seed(3)
-    rc = router(256, 8, groups, kept, group_score, score)
+    rc = router(E, K, groups, kept, group_score, score)
     for dtype in (torch.float32, torch.bfloat16):
-        x = torch.randint(-2, 3, (300, 256), generator=g, device=DEV).to(dtype)
+        x = torch.randint(-2, 3, (300, E), generator=g, device=DEV).to(dtype)
         x[0] = 0.0
         x[1, ::2] = -0.0
         x[2] = 7.0
-        for bias in (None, torch.zeros(256, device=DEV), torch.randint(0, 2, (256,), generator=g, device=DEV) * 0.125):
+        for bias in (None, torch.zeros(E, device=DEV), torch.randint(0, 2, (E,), generator=g, device=DEV) * 0.125):
             check_route(rc, x, bias)
 
 
@@ -139,16 +157,17 @@ def test_route_orders_scores_that_fp32_merges():
     x = (x.view(torch.int32) + step.int()).view(torch.float32)
     bias = (0.5 - torch.sigmoid(base.double())).float()
     for groups, kept, gscore in ((1, 1, "max"), (8, 4, "top2"), (8, 4, "max")):
-        check_route(router(E, 8, groups, kept, gscore, "sigmoid"), x, bias)
+        for K in (8, 12):
+            check_route(router(E, K, groups, kept, gscore, "sigmoid"), x, bias)
     p = torch.softmax(base.double(), 0)
     check_route(router(E, 8, 1, 1, "max", "softmax"), x, (0.01 - p).float())
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("E,groups,kept", [(256, 1, 1), (256, 8, 2), (61, 1, 1), (1000, 8, 2)])
-def test_route_masked_infinite_and_nan_logits(score, E, groups, kept):
+@pytest.mark.parametrize("E,groups,kept,K", [(256, 1, 1, 8), (256, 8, 2, 8), (61, 1, 1, 8), (1000, 8, 2, 8),
+                                             (256, 8, 2, 11), (61, 1, 1, 16), (204, 4, 2, 8), (312, 8, 3, 10)])
+def test_route_masked_infinite_and_nan_logits(score, E, groups, kept, K):
     g = torch.Generator(device=DEV).manual_seed(5)
-    K = 8
     x = torch.randn(24, E, generator=g, device=DEV)
     inf = float("inf")
     x[0] = -inf                       # nothing to choose
