@@ -103,16 +103,15 @@ template <typename IO, int LPR>
 ep_status launch_route_backward_lanes(const RouteBwdArgs& a, hipStream_t s) {
   constexpr int kRows = kWave / LPR, V = 16 / sizeof(typename IO::type);
   const bool dense = !a.sigmoid && !a.renorm;
-  const int vec = a.E % V == 0 && !misaligned(a.grad, 16) &&
-                  (!dense || (a.stride % V == 0 && !misaligned(a.logits, 16)));
+  const int vec = a.E % V == 0;
   const size_t lds = (size_t)kRows * a.E * sizeof(float);
   const int blocks = (int)std::min<int64_t>((a.T + kRows - 1) / kRows, 16 * kCUs);
   const int pieces = (a.E / V + LPR - 1) / LPR;  // of a row, a lane
-  if (dense && vec && pieces <= 2)
+  if (dense && pieces <= 2)
     route_backward_lanes_kernel<IO, LPR, 2><<<blocks, kWave, lds, s>>>(a, vec);
-  else if (dense && vec && pieces <= 4)
+  else if (dense && pieces <= 4)
     route_backward_lanes_kernel<IO, LPR, 4><<<blocks, kWave, lds, s>>>(a, vec);
-  else if (dense && vec && pieces <= 8)
+  else if (dense && pieces <= 8)
     route_backward_lanes_kernel<IO, LPR, 8><<<blocks, kWave, lds, s>>>(a, vec);
   else
     route_backward_lanes_kernel<IO, LPR, 0><<<blocks, kWave, lds, s>>>(a, vec);

@@ -75,10 +75,10 @@ struct F32 {
     return m;
   }
   static __device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return m; }
-  // 16 bytes of values
+  // 16 bytes of values, to any address
   static __device__ __forceinline__ void store_piece(float* p, const float* v) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)p);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), (piece*)p);
   }
   // eight values to any address
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
@@ -110,7 +110,7 @@ struct Bf16 {
   }
   static __device__ __forceinline__ void store_piece(uint16_t* p, const float* v) {
     __builtin_nontemporal_store(u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                      pack_bf16x2(v[6], v[7])}, (u32x4*)p);
+                                      pack_bf16x2(v[6], v[7])}, (piece*)p);
   }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     *(u32x4_at2*)((uint16_t*)p + i) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
@@ -138,8 +138,9 @@ struct F16 {
   }
   static __device__ __forceinline__ void store_piece(uint16_t* p, const float* v) {
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-    __builtin_nontemporal_store(f16x8{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3], (_Float16)v[4],
-                                      (_Float16)v[5], (_Float16)v[6], (_Float16)v[7]}, (f16x8*)p);
+    const f16x8 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3],
+                     (_Float16)v[4], (_Float16)v[5], (_Float16)v[6], (_Float16)v[7]};
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), (piece*)p);
   }
   static __device__ __forceinline__ void store8(void* p, int64_t i, const float* v) {
     typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -908,7 +909,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
 // zeros in LDS, the rows go out in 16-byte pieces, and the terms are taken out
 // again, so that the zeros are written to LDS once for all rows of a wave.
 // NCH > 0: the dense form with a lane's NCH pieces of the row in registers, read
-// and raised once; 0: every other case.
+// and raised once; 0: every other case (vec: dense rows of whole pieces).
 template <typename IO, int LPR, int NCH>
 __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArgs a, int vec) {
   constexpr int kRows = kWave / LPR;
@@ -937,21 +938,28 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
     const float x = have ? clean_logit(IO::load_nt(a.logits, base + at)) : kNegInf;
     // softmax over the whole row: maximum and sum in one pass
     float m = kNegInf, sum = 0.0f;
-    float e[NCH > 0 ? NCH : 1][V];
+    float e[NCH > 0 ? NCH : 1][V], rest = kNegInf;
+    const int last = a.E / V * V + l;  // fewer than V <= LPR values are no whole piece
     if (NCH > 0) {
-      const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+      const typename IO::type* src = (const typename IO::type*)a.logits + base;
       bool nan = false;
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const int c = j * LPR + l;
         const bool in = c < a.E / V;
-        IO::unpack(src[in ? c : 0], e[j]);
+        IO::unpack(!in ? u32x4{0, 0, 0, 0} : *(const typename IO::piece*)(src + c * V), e[j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           nan |= in && e[j][i] != e[j][i];
           e[j][i] = in ? clean_logit(e[j][i]) : kNegInf;
           m = fmaxf(m, e[j][i]);
         }
+      }
+      if (a.E % V != 0 && last < a.E) {
+        const float x = IO::load(a.logits, base + last);
+        nan |= x != x;
+        rest = clean_logit(x);
+        m = fmaxf(m, rest);
       }
       m = fmaxf(lanes_max<LPR>(m), -3.402823466e38f);  // finite, also in a row of -Inf
 #pragma unroll
@@ -961,6 +969,8 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
           e[j][i] = fast_exp(e[j][i] - m);
           sum += e[j][i];
         }
+      rest = fast_exp(rest - m);
+      sum += rest;
       sum = lanes_sum<LPR>(nan ? __uint_as_float(0x7FC00000u) : sum);
     } else if (dense) {
       auto add = [&](const float* f, int n) {
@@ -977,10 +987,10 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
         m = top;
       };
       if (vec) {
-        const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+        const typename IO::type* src = (const typename IO::type*)a.logits + base;
         for (int c = l; c < a.E / V; c += LPR) {
           float f[V];
-          IO::unpack(src[c], f);
+          IO::unpack(*(const typename IO::piece*)(src + c * V), f);
           add(f, V);
         }
       } else {
@@ -1040,9 +1050,9 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
     }
     if (first) row_terms[at] = total;
     wave_sync();
-    if (NCH == 0 && !dense && vec) {
-      // rows are neighbours in memory: the wave writes them as one piece
-      const int pieces = (int)min((int64_t)kRows, a.T - row0) * (a.E / V);
+    if (NCH == 0 && !dense) {
+      // rows are neighbours in memory: the wave writes them as one
+      const int n = (int)min((int64_t)kRows, a.T - row0) * a.E, pieces = n / V;
       typename IO::type* dst = (typename IO::type*)a.grad + row0 * a.E;
       for (int c = lane; c < pieces; c += kWave) {
         float f[V];
@@ -1050,9 +1060,10 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
         for (int i = 0; i < V; ++i) f[i] = terms[c * V + i];
         IO::store_piece(dst + c * V, f);
       }
+      if (pieces * V + lane < n) IO::store(a.grad, row0 * a.E + pieces * V + lane, terms[pieces * V + lane]);
     } else if (live) {
       const bool any = inner != 0.0f || (ballot(have) >> (lane - l) & (LPR == 16 ? 0xFFFFull : 0xFFull)) != 0;
-      const float back = dense && any ? -inner / sum : 0.0f;  // (a token without a choice: zeros, whatever its logits)
+      const float back = any ? -inner / sum : 0.0f;  // (a token without a choice: zeros, whatever its logits)
       if (NCH > 0) {
         typename IO::type* dst = (typename IO::type*)a.grad + row * a.E;
 #pragma unroll
@@ -1064,15 +1075,17 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
           for (int i = 0; i < V; ++i) t[i] = row_terms[c * V + i] + (any ? back * e[j][i] : 0.0f);
           IO::store_piece(dst + c * V, t);
         }
+        if (a.E % V != 0 && last < a.E)
+          IO::store(a.grad, row * a.E + last, row_terms[last] + (any ? back * rest : 0.0f));
       } else if (vec) {
-        const u32x4* src = (const u32x4*)((const typename IO::type*)a.logits + base);
+        const typename IO::type* src = (const typename IO::type*)a.logits + base;
         typename IO::type* dst = (typename IO::type*)a.grad + row * a.E;
         for (int c = l; c < a.E / V; c += LPR) {
           float f[V], t[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) t[i] = row_terms[c * V + i];
           if (any) {
-            IO::unpack(src[c], f);
+            IO::unpack(*(const typename IO::piece*)(src + c * V), f);
 #pragma unroll
             for (int i = 0; i < V; ++i) t[i] += back * expf(clean_logit(f[i]) - m);
           }
@@ -1081,7 +1094,7 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
       } else {
         for (int e = l; e < a.E; e += LPR) {
           float t = row_terms[e];
-          if (dense && any) t += back * expf(clean_logit(IO::load(a.logits, base + e)) - m);
+          if (any) t += back * expf(clean_logit(IO::load(a.logits, base + e)) - m);
           IO::store(a.grad, row * a.E + e, t);
         }
       }

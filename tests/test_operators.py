@@ -243,6 +243,28 @@ def test_route_backward_matches_the_formula(score, renorm, E, K):
         assert_close(f64(dx), ref, tol, "grad")
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False)])
+@pytest.mark.parametrize("E,K", [(61, 4), (137, 12), (256, 8), (600, 6), (1030, 5)])
+def test_route_backward_at_any_address(dtype, score, renorm, E, K):
+    """Logits and gradients that start at any element, nothing written beside them."""
+    g = torch.Generator(device=DEV).manual_seed(E + K)
+    T = 43
+    rc = router(E, K, score=score, renormalize=renorm)
+    x = torch.randn(T, E, generator=g, device=DEV).to(DTYPES[dtype])
+    idx, _ = ep.route(rc, x)
+    gw = torch.randn(T, K, generator=g, device=DEV)
+    want = ep.route_backward(rc, x, idx, gw)
+    for off in (1, 3):
+        rows = torch.empty(T * (E + 3) + off, dtype=DTYPES[dtype], device=DEV)[off:].view(T, E + 3)[:, :E]
+        rows.copy_(x)
+        store = torch.full((T * E + 32,), 9.0, dtype=DTYPES[dtype], device=DEV)
+        grad = store[off:off + T * E].view(T, E)
+        ep.route_backward(rc, rows, idx, gw, out=grad)
+        assert torch.equal(grad, want)
+        assert (store[:off] == 9.0).all() and (store[off + T * E:] == 9.0).all()
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route_backward_matches_differences(score, renorm):
