@@ -190,11 +190,7 @@ ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
 //    tiles of 128 x 256 while they fill three eighths (2048 x 7168 x 4096 gated: 67
 //    against 82 us; 8192 x 8192 x 8192: 256 x 256 by 10%);
 //  - below that, or for at most 64 rows, the split over the inner size (512 x 7168
-//    x 4096 gated: 29 us against 54 and 79; 64 rows: 11 against 44 and 49).
-//    Row tiles of 16, 32 or 64 by the rows there are.  Two waves a workgroup leave
-//    room for several workgroups a CU; four are better where the inner size is long
-//    and the grid at most one workgroup a CU (one row: 11 against 17 us), or one row tile of 16 (32
-//    groups of 3 rows, inner 7168: 150 against 155 us; inner 1024: 97 against 82).
+//    x 4096 gated: 23 us against 54 and 79; 64 rows: 9 against 44 and 49).
 // Groups: their sizes are on the device.  A group of at most kFewRows rows is
 // the split's and a larger one the tiles'; each launch passes over the others'
 // groups.  No second launch where large groups cannot be many enough to fill the
@@ -202,15 +198,45 @@ ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
 // one where the mean is so large that few groups are small.
 constexpr int64_t kFewRows = 64;
 
+// The split's tile, MT x NT sixteens of rows and channels.  Its time is that of the
+// loads, MT + NT for each step of a workgroup, on the CU with the most workgroups:
+// the shape for which that is least.  1 x 7168 x 4096 gated: 1 x 2 7.4 us, 1 x 4 9.0;
+// 64 rows: 2 x 2 9.0, 1 x 2 10.5, 2 x 4 9.8, 4 x 4 12.6; 512 rows: 4 x 4 23, 2 x 4 35;
+// 3475 x 6432 x 99: 2 x 4 14, 4 x 4 18.
+// Two waves a workgroup leave room for several workgroups a CU.  Four are better
+// where weights that no cache holds stream through a long inner size (one row: 7.4
+// against 9.4 us; 32 groups of 3 rows: 154 against 160; from the L2, 8 groups of 79
+// rows, 3904 x 78: 9.3 against 7.1) and a CU has one workgroup or small ones (512
+// rows, two a CU: 27 against 23).
+template <typename IO, bool GATED, int MT, int NT>
+ep_status launch_matmul_split(const MatmulArgs& a, int64_t blocks, hipStream_t s) {
+  const bool stream = a.K >= 2048 && (int64_t)a.G * a.N * a.K >= (int64_t)8 << 20;
+  return stream && (MT == 1 || blocks <= kCUs) ? launch_matmul_split<IO, GATED, MT, NT, 4, 2>(a, s)
+                                               : launch_matmul_split<IO, GATED, MT, NT, 2, 2>(a, s);
+}
+
 template <typename IO, bool GATED>
-ep_status launch_matmul_few(const MatmulArgs& a, int64_t mean, hipStream_t s) {
-  if (mean <= 16)
-    return a.K >= 2048 ? launch_matmul_split<IO, GATED, 1, 4, 4, 2>(a, s)
-                       : launch_matmul_split<IO, GATED, 1, 4, 2, 2>(a, s);
-  if (mean <= 32) return launch_matmul_split<IO, GATED, 2, 4, 2, 2>(a, s);
-  const int64_t blocks = (a.M + 63) / 64 * ((a.width + 31) / 32);
-  if (a.K >= 4096 && blocks <= kCUs) return launch_matmul_split<IO, GATED, 4, 4, 4, 2>(a, s);
-  return launch_matmul_split<IO, GATED, 4, 4, 2, 2>(a, s);
+ep_status launch_matmul_few(const MatmulArgs& a, hipStream_t s) {
+  constexpr int kShapes[5][2] = {{1, 2}, {1, 4}, {2, 2}, {2, 4}, {4, 4}};
+  const int64_t mean = std::min(a.M / a.G + (a.M % a.G != 0), a.most);
+  int64_t least = INT64_MAX, blocks = 0;
+  int best = 0;
+  for (int i = 0; i < 5; ++i) {
+    const int rows = 16 * kShapes[i][0], cols = (GATED ? 8 : 16) * kShapes[i][1];
+    const int64_t n = (mean + rows - 1) / rows * a.G * ((a.width + cols - 1) / cols);
+    const int64_t cost = (n + kCUs - 1) / kCUs * (kShapes[i][0] + kShapes[i][1]);
+    if (cost > least) continue;  // (of equals the larger one)
+    least = cost;
+    blocks = n;
+    best = i;
+  }
+  switch (best) {
+    case 0: return launch_matmul_split<IO, GATED, 1, 2>(a, blocks, s);
+    case 1: return launch_matmul_split<IO, GATED, 1, 4>(a, blocks, s);
+    case 2: return launch_matmul_split<IO, GATED, 2, 2>(a, blocks, s);
+    case 3: return launch_matmul_split<IO, GATED, 2, 4>(a, blocks, s);
+    default: return launch_matmul_split<IO, GATED, 4, 4>(a, blocks, s);
+  }
 }
 
 template <typename IO, bool GATED>
@@ -223,15 +249,15 @@ ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
     if ((a.M + 255) / 256 * n_tiles >= 3 * kCUs / 4) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
     if (a.M > kFewRows && (a.M + 127) / 128 * n_tiles >= 3 * kCUs / 8)
       return launch_matmul_tile<IO, GATED, 128, 256, 2, 4, false>(a, s);
-    return launch_matmul_few<IO, GATED>(a, a.M, s);
+    return launch_matmul_few<IO, GATED>(a, s);
   }
   const int64_t mean = a.M / a.G;
   const int64_t large = std::min<int64_t>(a.G, a.M / (kFewRows + 1));
-  if ((a.M / 256 + large) * n_tiles < 3 * kCUs / 8) return launch_matmul_few<IO, GATED>(a, mean, s);
+  if ((a.M / 256 + large) * n_tiles < 3 * kCUs / 8) return launch_matmul_few<IO, GATED>(a, s);
   if (mean < 4 * kFewRows) {
     MatmulArgs few = a;
     few.most = kFewRows;
-    const ep_status st = launch_matmul_few<IO, GATED>(few, mean, s);
+    const ep_status st = launch_matmul_few<IO, GATED>(few, s);
     if (st != EP_OK) return st;
     a.least = kFewRows + 1;
   }

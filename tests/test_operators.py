@@ -458,6 +458,28 @@ def test_product_dense_matches_plain(M, K, N, gated):
         check_product(g, M, K, N + 1, None, None, gated, torch.bfloat16)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,K,width", [
+    (1, 2048, 4091), (5, 2064, 16384), (40, 2048, 4091), (64, 2048, 8190), (250, 2304, 4093),  # streams of weights
+    (300, 208, 8188), (600, 208, 16385),                                                       # tiles
+])
+def test_product_wide_matches_plain(M, K, width, gated):
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    N = width * (2 if gated else 1)
+    a, w = codes(g, M, K), codes(g, N, K)
+    sa = (torch.rand(M, generator=g, device=DEV) + 0.5) * 2.0 ** -7
+    sw = (torch.rand(N, generator=g, device=DEV) + 0.5) * 2.0 ** -7 / K ** 0.5
+    ref = f64(a.double() @ w.double().t().contiguous()) * f64(sa)[:, None] * f64(sw)[None, :]  # (sums below 2^53: exact)
+    gate = None
+    if gated:
+        gate, up = ref[:, :width], ref[:, width:]
+        ref = plain.silu(gate) * up
+    for dtype in (torch.bfloat16, torch.float32):
+        say("product wide", M, K, width, gated, dtype)
+        got = ep.matmul_int8((a, sa), (w, sw), gated=gated, out_dtype=dtype)
+        assert_close(f64(got), ref, product_tolerance(ref, gate, dtype), "product")
+
+
 GROUPED = [
     # counts, alignment of the starts, spare rows at the end
     ([3], 1, 0),
