@@ -706,9 +706,10 @@ ep_status ep_route(const ep_route_config* cfg, int32_t type, const void* logits,
   if (misaligned(logits, type_bytes(type)) || misaligned(bias, 4) || misaligned(topk_idx, 8) ||
       misaligned(topk_weights, 4))
     return fail(EP_ERR_SHAPE, "logits / bias / topk_idx / topk_weights must be aligned to their element size");
+  const bool grouped = cfg->topk_groups < cfg->num_groups;  // groups that are all kept decide nothing
   RouteArgs a{logits, row_stride, bias, token_mask, topk_idx, topk_weights, (int)num_tokens, cfg->num_experts,
-              cfg->num_topk, cfg->num_groups, cfg->topk_groups, cfg->score == EP_SCORE_SIGMOID,
-              cfg->group_score == EP_GROUP_TOP2, cfg->renormalize != 0, cfg->scale};
+              cfg->num_topk, grouped ? cfg->num_groups : 1, grouped ? cfg->topk_groups : 1,
+              cfg->score == EP_SCORE_SIGMOID, cfg->group_score == EP_GROUP_TOP2, cfg->renormalize != 0, cfg->scale};
   return with_type(type, [&](auto io) { return launch_route<decltype(io)>(a, (hipStream_t)stream); });
 }
 

@@ -161,24 +161,41 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Value of lane (lane ^ X), X < 16, by DPP.
+template <int X>
+__device__ __forceinline__ int xor_lane(int v) {
+  if constexpr (X >= 8) return xor_lane<15 ^ X>(__builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));  // mirror of 16
+  else if constexpr (X >= 4) return xor_lane<7 ^ X>(__builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));  // mirror of 8
+  else if constexpr (X == 3) return __builtin_amdgcn_mov_dpp(v, 0x1B, 0xF, 0xF, true);
+  else if constexpr (X == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (X == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
+  else return v;
+}
+template <int X>
+__device__ __forceinline__ float xor_lane(float v) { return __int_as_float(xor_lane<X>(__float_as_int(v))); }
+template <int X>
+__device__ __forceinline__ double xor_lane(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)xor_lane<X>((int)(uint32_t)b) |
+                                        (uint64_t)(uint32_t)xor_lane<X>((int)(uint32_t)(b >> 32)) << 32);
+}
+
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_max(double v) {
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-  return v;
+  v = fmax(v, xor_lane<1>(v));
+  v = fmax(v, xor_lane<2>(v));
+  v = fmax(v, xor_lane<7>(v));
+  v = fmax(v, xor_lane<15>(v));
+  return fmax(fmax(lane_value(v, 0), lane_value(v, 16)), fmax(lane_value(v, 32), lane_value(v, 48)));
 }
 __device__ __forceinline__ double wave_sum(double v) {
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
-}
-
-// Largest (key, lowest index) over the wave; idx < 0 where a lane has none.
-__device__ __forceinline__ void wave_best(double& key, int& idx) {
-  for (int o = 32; o > 0; o >>= 1) {
-    const double k2 = __shfl_xor(key, o, 64);
-    const int i2 = __shfl_xor(idx, o, 64);
-    const bool take = i2 >= 0 && (idx < 0 || k2 > key || (k2 == key && i2 < idx));
-    key = take ? k2 : key;
-    idx = take ? i2 : idx;
-  }
 }
 
 // One row by one wave, all in 64 bits.  key: E doubles of LDS that the wave
@@ -198,22 +215,25 @@ __device__ void route_row(const RouteArgs& a, int64_t row, double* key) {
   }
   const bool any_nan = ballot(nan) != 0;
   m = wave_max(m);
+  // keys; -Inf marks an expert that cannot be chosen
   double sum = 1.0;
-  if (!a.sigmoid && (!by_logit || !a.renorm)) {
+  const bool soft = !a.sigmoid && (!by_logit || !a.renorm);
+  if (soft) {
     sum = 0.0;
     for (int e = lane; e < a.E; e += kWave) {
       const float x = IO::load(a.logits, base + e);
-      if (x > kNegInf) sum += exp((double)clean_logit(x) - m);
+      const double p = x > kNegInf ? exp((double)clean_logit(x) - m) : 0.0;
+      sum += p;
+      key[e] = p;
     }
     sum = wave_sum(sum);
   }
-  // keys; -Inf marks an expert that cannot be chosen
   for (int e = lane; e < a.E; e += kWave) {
     const float x = IO::load(a.logits, base + e);
     double k = -__builtin_inf();
     if (x > kNegInf) {
       const double v = (double)clean_logit(x);
-      k = by_logit ? v : a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - m) / sum;
+      k = by_logit ? v : a.sigmoid ? 1.0 / (1.0 + exp(-v)) : key[e] / sum;
       if (a.bias) k += (double)a.bias[e];
       if (!(k > -__builtin_inf())) k = -__builtin_inf();
     }
@@ -226,14 +246,11 @@ __device__ void route_row(const RouteArgs& a, int64_t row, double* key) {
     double s = -__builtin_inf();
     if (lane < a.G) {
       double m1 = -__builtin_inf(), m2 = -__builtin_inf();
+#pragma unroll 4
       for (int i = 0; i < gs; ++i) {
         const double k = key[lane * gs + i];
-        if (k > m1) {
-          m2 = m1;
-          m1 = k;
-        } else if (k > m2) {
-          m2 = k;
-        }
+        m2 = fmax(m2, fmin(m1, k));
+        m1 = fmax(m1, k);
       }
       s = a.top2 && m2 > -__builtin_inf() ? m1 + m2 : m1;
     }
@@ -248,22 +265,34 @@ __device__ void route_row(const RouteArgs& a, int64_t row, double* key) {
       if (!((keep >> (e / gs)) & 1)) key[e] = -__builtin_inf();
     wave_sync();
   }
+  // Every lane has the best of its experts at hand; the best lane gives its up and
+  // looks for its next.
   int mine = -1;  // lane j holds choice j
-  for (int j = 0; j < a.K; ++j) {
-    double best = -__builtin_inf();
-    int at = -1;
+  double best;
+  int at;
+  auto look = [&]() {
+    best = -__builtin_inf();
+    at = -1;
+#pragma unroll 4
     for (int e = lane; e < a.E; e += kWave) {
       const double k = key[e];
-      if (k > best) {
-        best = k;
-        at = e;
-      }
+      at = k > best ? e : at;
+      best = fmax(best, k);
     }
-    wave_best(best, at);
-    if (at < 0) break;
-    if (lane == j) mine = at;
-    if (lane == 0) key[at] = -__builtin_inf();
-    wave_sync();
+  };
+  look();
+  for (int j = 0; j < a.K; ++j) {
+    const double top = wave_max(best);
+    if (!(top > -__builtin_inf())) break;
+    uint64_t tied = ballot(best == top);
+    int first = __builtin_amdgcn_readlane(at, __builtin_ctzll(tied));
+    for (tied &= tied - 1; tied; tied &= tied - 1)
+      first = min(first, __builtin_amdgcn_readlane(at, __builtin_ctzll(tied)));
+    if (lane == j) mine = first;
+    if (at == first) {
+      key[first] = -__builtin_inf();
+      look();
+    }
   }
   // Weights.  Renormalised ones are formed relative to the largest chosen
   // score, so that their sum neither overflows nor vanishes:
@@ -311,8 +340,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // order is that of the floats (all of them finite doubles, -Inf included), with
 // the expert in the low word (inverted for positive keys): one v_max_f64 and one
 // v_min_f64 exchange key and expert, and equal keys stand in the order of the
-// experts.  (Scores skip the inversion by sign, two operations a key: a row whose
-// last choice has a negative key is done over.)  A lane sorts eights of its keys, keeps the best eight, and three or
+// experts.  (Waves without a negative key skip the inversion by sign, two operations
+// a key.)  A lane sorts eights of its keys, keeps the best eight, and three or
 // four bitonic merges over its neighbours leave the row's best eight in every lane.
 // More than eight choices (R = 2) take a second round over the keys below the eighth
 // (65536 x 256 bf16, top 10: 28 us, against 178 with one row a wave in 64 bits).
@@ -322,25 +351,6 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // and the best expert left out, or a kept and a dropped group, lie within the
 // error of the fp32 scores (and are not equal for being made of equal numbers)
 // is done over in 64 bits by the whole wave (route_row), about one row in 500.
-
-// Value of lane (lane ^ X), X < 16, by DPP.
-template <int X>
-__device__ __forceinline__ int xor_lane(int v) {
-  if constexpr (X >= 8) return xor_lane<15 ^ X>(__builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));  // mirror of 16
-  else if constexpr (X >= 4) return xor_lane<7 ^ X>(__builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));  // mirror of 8
-  else if constexpr (X == 3) return __builtin_amdgcn_mov_dpp(v, 0x1B, 0xF, 0xF, true);
-  else if constexpr (X == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
-  else if constexpr (X == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
-  else return v;
-}
-template <int X>
-__device__ __forceinline__ float xor_lane(float v) { return __int_as_float(xor_lane<X>(__float_as_int(v))); }
-template <int X>
-__device__ __forceinline__ double xor_lane(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)(uint32_t)xor_lane<X>((int)(uint32_t)b) |
-                                        (uint64_t)(uint32_t)xor_lane<X>((int)(uint32_t)(b >> 32)) << 32);
-}
 
 // Over the N (8 or 16) lanes of a row; every lane gets the result.
 template <int N>
@@ -428,16 +438,18 @@ __device__ __forceinline__ int expert_of(double d, int by_sign) {
   return ~((int)(uint32_t)b ^ (((int)(uint32_t)(b >> 32) >> 31) & by_sign));
 }
 
-// The best eight of a lane's keys, falling; BELOW: of those that come after `limit`.
-template <int VPL, bool BY_SIGN, bool BELOW>
-__device__ __forceinline__ void best_of_lane(const float (&key)[VPL], int e0, double limit, double (&list)[8]) {
+// The best eight of a lane's keys, falling, in rounds after the first of those that
+// come after list[7].
+template <int VPL, bool BY_SIGN>
+__device__ __forceinline__ void best_of_lane(const float (&key)[VPL], int e0, int round, double (&list)[8]) {
+  const double limit = list[7];
 #pragma unroll
   for (int c = 0; c < VPL; c += 8) {
     double v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = tagged<BY_SIGN>(key[c + i], e0 + c + i);
-      if (BELOW) v[i] = v[i] < limit ? v[i] : tagged<true>(kNegInf, 0);
+      if (round > 0) v[i] = v[i] < limit ? v[i] : tagged<true>(kNegInf, 0);
     }
     sort8(v);
     if (c == 0) {
@@ -493,6 +505,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   const int have = group < a.G ? max(0, min(p.seg, p.gs - share * p.seg)) : 0;
   const float* const mine = row_lds + (p.pitch ? l * p.pitch : have > 0 ? e0 : 0);
   const bool by_logit = !a.bias && (a.G == 1 || !a.top2);
+  bool by_sign = by_logit;  // keys below zero stand in order too
 
   // logits to LDS
   constexpr int V = 16 / sizeof(typename IO::type);
@@ -594,7 +607,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       for (int i = 0; i < VPL; ++i) key[i] = i < have ? key[i] : kNegInf;
     }
     if (a.bias) {
-      float best = kNegInf;
+      float best = kNegInf, worst = 0.0f;
       if (p.bias_vec) {
 #pragma unroll
         for (int i = 0; i < VPL; i += 4) {
@@ -619,6 +632,9 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
 #pragma unroll
       for (int i = 0; i < VPL; i += 2)
         best = __builtin_elementwise_maximum(__builtin_elementwise_maximum(best, key[i]), key[i + 1]);
+#pragma unroll
+      for (int i = 0; i < VPL; i += 2) worst = fminf(fminf(worst, key[i]), key[i + 1]);
+      by_sign = ballot(worst < 0.0f) != 0;
       // a key of -Inf or NaN cannot be chosen; one of +Inf is decided in 64 bits
       if (ballot(!(best < __builtin_inff()))) {
 #pragma unroll
@@ -692,18 +708,10 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
   double mine_d[R];  // lane l < 8 of the row holds choices l, l + 8, ..
 #pragma unroll
   for (int c = 0; c < R; ++c) {
-    if (c == 0) {
-      if (by_logit)
-        best_of_lane<VPL, true, false>(key, e0, none, list);
-      else
-        best_of_lane<VPL, false, false>(key, e0, none, list);
-    } else {
-      const double limit = list[7];
-      if (by_logit)
-        best_of_lane<VPL, true, true>(key, e0, limit, list);
-      else
-        best_of_lane<VPL, false, true>(key, e0, limit, list);
-    }
+    if (by_sign)
+      best_of_lane<VPL, true>(key, e0, c, list);
+    else
+      best_of_lane<VPL, false>(key, e0, c, list);
 #pragma unroll
     for (int i = 0; i < 8; ++i) own[i] = list[i] = lane_kept ? list[i] : none;
     merge8_lane<1>(list);
@@ -721,7 +729,7 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
 #pragma unroll
   for (int c = 0; c < R; ++c) {
     chosen[c] = (R == 1 || l < 8) && c * 8 + l < a.K && key_of(mine_d[c]) > kNegInf;
-    e[c] = chosen[c] ? expert_of(mine_d[c], by_logit ? -1 : 0) : 0;
+    e[c] = chosen[c] ? expert_of(mine_d[c], by_sign ? -1 : 0) : 0;
     x[c] = chosen[c] ? clean_logit(*place(e[c])) : kNegInf;
   }
 
@@ -729,7 +737,6 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     float kf[R], b[R], largest = 0.0f;
 #pragma unroll
     for (int c = 0; c < R; ++c) {
-      unsure |= chosen[c] && key_of(mine_d[c]) < 0.0f;
       kf[c] = chosen[c] ? key_of(mine_d[c]) : 0.0f;
       b[c] = a.bias && chosen[c] ? a.bias[e[c]] : 0.0f;
       largest = fmaxf(largest, fabsf(kf[c]));

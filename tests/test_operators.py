@@ -86,6 +86,8 @@ ROUTERS = [
     (72, 8, 8, 8, "max"),
     (239, 8, 1, 1, "max"),
     (137, 6, 1, 1, "max"),
+    (9, 9, 1, 1, "max"),
+    (128, 8, 4, 4, "top2"),
 ]
 
 
@@ -140,7 +142,8 @@ def test_route_ties_go_to_the_lowest_expert(score, groups, kept, group_score, E,
         x[0] = 0.0
         x[1, ::2] = -0.0
         x[2] = 7.0
-        for bias in (None, torch.zeros(E, device=DEV), torch.randint(0, 2, (E,), generator=g, device=DEV) * 0.125):
+        for bias in (None, torch.zeros(E, device=DEV), torch.randint(0, 2, (E,), generator=g, device=DEV) * 0.125,
+                     torch.randint(-3, 1, (E,), generator=g, device=DEV) * 0.5):  # keys below zero
             check_route(rc, x, bias)
 
 
