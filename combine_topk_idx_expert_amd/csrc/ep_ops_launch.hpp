@@ -194,9 +194,10 @@ ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
 // Groups: their sizes are on the device.  A group of at most kFewRows rows is
 // the split's and a larger one the tiles'; each launch passes over the others'
 // groups.  No second launch where large groups cannot fill half of the tiles' grid
-// (8 groups of 72 rows, 7168 x 4096 gated: 72 us by the split alone, 84 by both; 4 of
-// 130: 44 against 53), nor a first one where the mean is so large that few groups
-// are small.
+// (8 groups of 72 rows, 7168 x 4096 gated: 72 us by the split alone, 84 by both), or
+// three eighths for tall groups, whose rows the split takes 64 at a time (8 of 1696,
+// 4672 x 318 gated: 46 us by tiles, 80 by the split); nor a first one where the mean
+// is so large that few groups are small.
 constexpr int64_t kFewRows = 64;
 
 // The split's tile, MT x NT sixteens of rows and channels.  Its time is that of the
@@ -255,7 +256,7 @@ ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
   const int64_t mean = a.M / a.G;
   // row tiles that large groups can fill: a tile has more than kFewRows rows
   const int64_t large = std::min(a.M / 256 + a.G, a.M / (kFewRows + 1));
-  if (large * n_tiles <= kCUs / 2) return launch_matmul_few<IO, GATED>(a, s);
+  if (large * n_tiles < (mean <= 2 * kFewRows ? kCUs / 2 + 1 : 3 * kCUs / 8)) return launch_matmul_few<IO, GATED>(a, s);
   if (mean < 4 * kFewRows) {
     MatmulArgs few = a;
     few.most = kFewRows;
