@@ -351,6 +351,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // and the best expert left out, or a kept and a dropped group, lie within the
 // error of the fp32 scores (and are not equal for being made of equal numbers)
 // is done over in 64 bits by the whole wave (route_row), about one row in 500.
+//
+// Vector instructions bound it, ~165 a row of 256 with groups and bias: 262144 rows
+// of fp32 in 92 us, 60% of the memory's rate; 32768 rows of bf16 by logits 9-10 us; one
+// row 5.3 us, a wave's latency.  One row a wave in 64 bits took 759 and 38 us.
 
 // Over the N (8 or 16) lanes of a row; every lane gets the result.
 template <int N>
@@ -914,7 +918,9 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
 // choice, in 32 bits.  What has to move is the gradient (and, with a softmax
 // that is not renormalised, the logits): the choices' terms are put into rows of
 // zeros in LDS, the rows go out in 16-byte pieces, and the terms are taken out
-// again, so that the zeros are written to LDS once for all rows of a wave.
+// again, so that the zeros are written to LDS once for all rows of a wave.  Memory
+// bounds it: 262144 x 256 fp32 in 80 us, of which the chosen logits, a line each, are
+// 25; dense, 131072 x 256 bf16 in 33 us, 4.3 TB/s (one row a wave: 189 and 179 us).
 // NCH > 0: the dense form with a lane's NCH pieces of the row in registers, read
 // and raised once; 0: every other case (vec: dense rows of whole pieces).
 template <typename IO, int LPR, int NCH>
