@@ -672,8 +672,10 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
     if (p.shift >= 2) join(xor_lane<2>(m1), xor_lane<2>(m2));
     if (p.shift >= 3) join(xor_lane<7>(m1), xor_lane<7>(m2));
     const int g = group;
-    // (groups past the last own nothing: -Inf, behind every other or tied with an empty one)
-    const float s = a.top2 && m2 > kNegInf ? m1 + m2 : m1;
+    // Groups past the last own nothing: -Inf, behind every other or tied with an empty one.
+    // A sum below fp32 (experts switched off by a bias of its lowest value) counts as the
+    // lowest value, before an empty group; two such sums are equal, and decided in 64 bits.
+    const float s = a.top2 && m2 > kNegInf ? fmaxf(m1 + m2, -3.402823466e38f) : m1;
     int ahead = 0;
     auto count = [&](float o, int ol) {
       const int og = ol >> p.shift;

@@ -1,0 +1,83 @@
+"""Routing and int8 operators at the borders of their number ranges, against plain 64-bit
+implementations: group sums beyond fp32, ties under a bias, rows without a choosable logit, NaN
+in the gradient, gates that close.
+
+Tolerances come from the number of roundings; u is half a step of fp32, 2^-24.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_topk_idx_expert_amd as ep
+import plain_operators as plain
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+LOWEST = torch.finfo(torch.float32).min
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def half_step(dtype):
+    return 0.0 if dtype == torch.float32 else torch.finfo(dtype).eps / 2
+
+
+def generator(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def check_ids(rc, x, bias):
+    idx, w = ep.route(rc, x, bias=bias)
+    ref_idx, ref_w = plain.route(rc, f64(x), None if bias is None else f64(bias))
+    np.testing.assert_array_equal(idx.cpu().numpy(), ref_idx)
+    # the exponential's argument is off by a few u for each unit of its size, the rest by a few u
+    top = np.abs(np.where(np.isfinite(f64(x)), f64(x), 0)).max()
+    np.testing.assert_allclose(f64(w), ref_w, rtol=(40 + rc.K + 8 * min(top, 110)) * U, atol=2.0 ** -125)
+    return idx
+
+
+# -------------------------------------------------------------------------------- routing
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,groups,kept", [(16, 6, 4, 2), (32, 10, 4, 2), (64, 8, 8, 2), (256, 8, 8, 4), (200, 12, 8, 4),
+                                             (512, 16, 8, 2), (320, 10, 64, 7), (128, 12, 16, 5),
+                                             (64, 10, 8, 2), (64, 8, 8, 1), (200, 12, 8, 1), (512, 16, 8, 1),
+                                             (320, 11, 64, 3), (4096, 32, 64, 1)])
+def test_route_groups_whose_sum_leaves_fp32(score, E, K, groups, kept):
+    """Experts switched off by a bias of the lowest fp32 value: the sum of two such keys lies below fp32, and
+    a group of them still comes before a group without a choosable expert."""
+    g = generator(E + K)
+    size = E // groups
+    rc = ep.RouteConfig(E=E, K=K, score=score, num_groups=groups, topk_groups=kept, group_score="top2")
+    x = torch.randn(40, E, generator=g, device=DEV)
+    live = kept - 1                                   # groups that are left as they are, at the end
+    x[:, :size] = -INF                                # the first group has no choosable expert
+    x[20:, size:2 * size] = -INF                      # nor has the second, in half of the rows
+    off = torch.randn(E, generator=g, device=DEV) * 0.01
+    for low in (LOWEST, -2.0e38, -1.0e38):
+        bias = off.clone()
+        bias[size:E - live * size] = low
+        check_ids(rc, x, bias)
+        if groups - live >= 4:                        # groups switched off by different amounts
+            bias[2 * size:3 * size] = 0.75 * low
+            check_ids(rc, x, bias)
+    for high in (3.0e38, torch.finfo(torch.float32).max):  # and sums above fp32
+        bias = off.clone()
+        bias[size:2 * size] = high
+        bias[E - size:] = 0.9 * high
+        check_ids(rc, x, bias)
