@@ -864,7 +864,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
   const bool dense = !a.sigmoid && !a.renorm;
   if (dense) {
     for (int e = lane; e < a.E; e += kWave) m = fmax(m, (double)clean_logit(IO::load(a.logits, base + e)));
-    m = wave_max(m);
+    m = fmax(wave_max(m), -3.402823466e38);  // finite, also in a row of -Inf
     sum = 0.0;
     for (int e = lane; e < a.E; e += kWave) sum += exp((double)clean_logit(IO::load(a.logits, base + e)) - m);
     sum = wave_sum(sum);
@@ -906,7 +906,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
     if (dense) {
       const float xe = IO::load(a.logits, base + e);
       v = (float)(-(double)a.scale * inner * (exp((double)clean_logit(xe) - m) / sum));
-      if (ballot(have) == 0) v = 0.0f;
+      if (ballot(have) == 0 || sum == 0.0) v = 0.0f;  // (a row of -Inf has no score)
     }
     buf[e] = v;
   }
@@ -1014,7 +1014,7 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
           add(f, 1);
         }
       }
-      const float top = lanes_max<LPR>(m);
+      const float top = fmaxf(lanes_max<LPR>(m), -3.402823466e38f);
       sum = lanes_sum<LPR>(m > kNegInf ? sum * expf(m - top) : sum);
       m = top;
     }
@@ -1078,7 +1078,8 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
       if (pieces * V + lane < n) IO::store(a.grad, row0 * a.E + pieces * V + lane, terms[pieces * V + lane]);
     } else if (live) {
       const bool any = inner != 0.0f || (ballot(have) >> (lane - l) & (LPR == 16 ? 0xFFFFull : 0xFFull)) != 0;
-      const float back = any ? -inner / sum : 0.0f;  // (a token without a choice: zeros, whatever its logits)
+      // a token without a choice gets zeros, whatever its logits, and so does a row of -Inf, which has no score
+      const float back = any && sum != 0.0f ? -inner / sum : 0.0f;
       if (NCH > 0) {
         typename IO::type* dst = (typename IO::type*)a.grad + row * a.E;
 #pragma unroll

@@ -81,3 +81,34 @@ def test_route_groups_whose_sum_leaves_fp32(score, E, K, groups, kept):
         bias[size:2 * size] = high
         bias[E - size:] = 0.9 * high
         check_ids(rc, x, bias)
+
+
+# ------------------------------------------------------------------- gradient of the router
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,K", GRADIENTS)
+def test_route_backward_of_rows_without_a_score(score, renorm, E, K):
+    """Ids that name logits of -Inf, in rows of nothing else and in ordinary ones: their scores are 0, and
+    nothing reaches them."""
+    g = generator(E * K)
+    for dtype in DTYPES.values():
+        x = torch.randn(9, E, generator=g, device=DEV).to(dtype)
+        idx = torch.rand(9, E, generator=g, device=DEV).argsort(1)[:, :K].contiguous()
+        gw = torch.randn(9, K, generator=g, device=DEV)
+        x[0] = -INF
+        x[1] = -INF
+        x[1, idx[1, 0]] = 0.5                         # one of the choices alone
+        x[2] = -INF
+        x[2, (set(range(E)) - set(idx[2].tolist())).pop()] = 0.5  # an expert that was not chosen
+        x[3].scatter_(0, idx[3], -INF)                # every choice
+        x[4, idx[4, K - 1]] = -INF
+        x[5] = torch.finfo(dtype).min
+        rc = ep.RouteConfig(E=E, K=K, score=score, renormalize=renorm, scale=2.5)
+        got = f64(ep.route_backward(rc, x, idx, gw))
+        ref = plain.route_backward(rc, f64(x), idx.cpu().numpy(), f64(gw))
+        ref[0] = 0.0
+        assert np.isfinite(got).all()
+        xs = np.where(np.abs(f64(x)) < 1e3, f64(x), 0)
+        tol = gradient_tolerance(xs, K, 2.5, f64(gw), ref, dtype)
+        assert (np.abs(got - ref) <= tol).all(), (dtype, np.abs(got - ref).max())
