@@ -864,7 +864,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
   const bool dense = !a.sigmoid && !a.renorm;
   if (dense) {
     for (int e = lane; e < a.E; e += kWave) m = fmax(m, (double)clean_logit(IO::load(a.logits, base + e)));
-    m = fmax(wave_max(m), -3.402823466e38);  // finite, also in a row of -Inf
+    m = fmax(wave_max(m), (double)-3.402823466e38f);  // finite, also in a row of -Inf
     sum = 0.0;
     for (int e = lane; e < a.E; e += kWave) sum += exp((double)clean_logit(IO::load(a.logits, base + e)) - m);
     sum = wave_sum(sum);
