@@ -839,7 +839,8 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
 //   softmax, renormalised: dx_j = w_j (g_j - sum g w / c)
 //   softmax:               dx_e = c p_e ([e chosen] g_e - sum g_j p_j), every e
 // Experts that were not chosen get 0 in the first three.  An expert named by
-// two slots of a token gets the sum of both slots' terms.
+// two slots of a token gets the sum of both slots' terms.  Logits of -Inf have
+// score 0; NaN (compared as "not <= -Inf") goes on into all that its score enters.
 template <typename IO>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(RouteBwdArgs a) {
   extern __shared__ float grad_lds[];
@@ -874,18 +875,18 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
     const double top = wave_max(have ? (double)x : -__builtin_inf());
     const double t = fmin(top, 0.0);
     double w = 0.0;
-    if (have && x > kNegInf)
+    if (have && !(x <= kNegInf))
       w = !a.sigmoid ? exp(x - top) : x > 0.0f ? 1.0 / (1.0 + exp(-(double)x)) : exp(x - t) / (1.0 + exp((double)x));
     const double total = wave_sum(w);
-    if (total > 0.0) w /= total;
+    if (total != 0.0) w /= total;
     const double mean = wave_sum(have ? g * w : 0.0);
     d = w * (g - mean) * a.scale;
     if (a.sigmoid) d /= 1.0 + exp((double)x);
   } else if (a.sigmoid) {
     const double s = 1.0 / (1.0 + exp(-(double)x));
-    d = have && x > kNegInf ? a.scale * g * s / (1.0 + exp((double)x)) : 0.0;
+    d = have && !(x <= kNegInf) ? a.scale * g * s / (1.0 + exp((double)x)) : 0.0;
   } else {
-    const double p = have && x > kNegInf ? exp(x - m) / sum : 0.0;
+    const double p = have && !(x <= kNegInf) ? exp(x - m) / sum : 0.0;
     d = a.scale * g * p;
     inner = wave_sum(have ? g * p : 0.0);
   }
@@ -1023,17 +1024,17 @@ __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArg
       const float top = lanes_max<LPR>(x);
       const float t = fminf(top, 0.0f);
       float w = 0.0f;
-      if (x > kNegInf)
+      if (!(x <= kNegInf))
         w = !a.sigmoid ? expf(x - top) : x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - t) / (1.0f + expf(x));
       const float total = lanes_sum<LPR>(w);
-      if (total > 0.0f) w /= total;
+      if (total != 0.0f) w /= total;
       const float mean = lanes_sum<LPR>(have ? g * w : 0.0f);
       d = w * (g - mean) * a.scale;
       if (a.sigmoid) d /= 1.0f + expf(x);
     } else if (a.sigmoid) {
-      if (x > kNegInf) d = a.scale * g / ((1.0f + expf(-x)) * (1.0f + expf(x)));
+      if (!(x <= kNegInf)) d = a.scale * g / ((1.0f + expf(-x)) * (1.0f + expf(x)));
     } else {
-      const float p = x > kNegInf ? expf(x - m) / sum : 0.0f;
+      const float p = !(x <= kNegInf) ? expf(x - m) / sum : 0.0f;
       d = a.scale * g * p;
       inner = a.scale * lanes_sum<LPR>(have ? g * p : 0.0f);
     }

@@ -377,6 +377,10 @@ ep_status ep_route(const ep_route_config *cfg, int32_t type, const void *logits,
  *   grad_weights  device, fp32 [num_tokens, K].
  *   grad_logits   device, [num_tokens, E] contiguous, of `type`; every element
  *                 is written (0 where nothing reaches a logit).
+ * A logit of -Inf has score 0 here too.  A NaN logit makes NaN of what its score
+ * enters: the whole row where a token with a choice has a softmax over it
+ * (without renormalize), the token's choices where it is one of them
+ * (renormalize), else its own gradient.
  * The choice itself has no gradient, and neither has the bias, which enters
  * nothing else.  num_groups, topk_groups and group_score are checked and not
  * used.  Errors as ep_route. */

@@ -122,3 +122,41 @@ def test_route_backward_of_rows_without_a_score(score, renorm, E, K):
         xs = np.where(np.abs(f64(x)) < 1e3, f64(x), 0)
         tol = gradient_tolerance(xs, K, 2.5, f64(gw), ref, dtype)
         assert (np.abs(got - ref) <= tol).all(), (dtype, np.abs(got - ref).max())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,K", GRADIENTS)
+def test_route_backward_shows_nan(score, renorm, E, K):
+    """A NaN logit makes NaN of what it reaches: the whole row where the softmax runs over it, the token's
+    choices where it is one of them and they are renormalised, itself alone otherwise."""
+    g = generator(E + K)
+    nan = float("nan")
+    for dtype in DTYPES.values():
+        x = torch.randn(8, E, generator=g, device=DEV).to(dtype)
+        idx = torch.rand(8, E, generator=g, device=DEV).argsort(1)[:, :K].contiguous()
+        gw = torch.randn(8, K, generator=g, device=DEV)
+        x[1, idx[1, 0]] = nan                         # a choice
+        x[2, idx[2, K - 1]] = nan
+        x[2, idx[2, 0]] = -INF                        # beside one of score 0
+        other = (set(range(E)) - set(idx[3].tolist())).pop()
+        x[3, other] = nan                             # no choice
+        x[4] = nan
+        x[5] = nan
+        idx[5] = -1                                   # a token that was not routed
+        idx[6, K - 1] = -1                            # an unused slot
+        x[6, idx[6, 0]] = nan
+        rc = ep.RouteConfig(E=E, K=K, score=score, renormalize=renorm)
+        dx = ep.route_backward(rc, x, idx, gw).cpu()
+        want = torch.zeros(8, E, dtype=torch.bool)
+        for r in range(8):
+            named = idx[r][idx[r] >= 0].cpu()
+            bad = torch.isnan(x[r]).cpu()
+            if score == "softmax" and not renorm:
+                want[r] = len(named) > 0 and bool(bad.any())
+            elif renorm:
+                want[r, named] = bool(bad[named].any())
+            else:
+                want[r, named] = bad[named]
+        assert torch.equal(torch.isnan(dx), want), (dtype, torch.isnan(dx).sum(1), want.sum(1))
+        assert (dx[5] == 0).all()
