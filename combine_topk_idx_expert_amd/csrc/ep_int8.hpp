@@ -198,12 +198,22 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& a, int g, int64_t& 
   if (hi - lo < a.least || hi - lo > a.most) hi = lo;
 }
 
-// For a 16-bit result the hardware's exp2 and reciprocal (a third of the
-// operations): the exponent's rounding makes a relative error below 2^-17, where
-// the result's own is 2^-9 or 2^-12.
+// g / (1 + exp(-g)).  Below -87 the quotient's denominator leaves fp32 while its value
+// does not, so neither form lets it grow so far.
+// For a 16-bit result the hardware's exp2 and reciprocal (a third of the operations),
+// of the denominator times 2^-16: the exponent's rounding makes a relative error below
+// 2^-17, where the result's own is 2^-9 or 2^-12; a score below 2^-142 is 0.
+// For fp32, 1 + exp(-g) is exp(-g) below -60, and half the exponent twice stays in range.
 template <typename IO>
 __device__ __forceinline__ float silu(float g) {
-  if (sizeof(typename IO::type) == 2) return g * __builtin_amdgcn_rcpf(1.0f + fast_exp(-g));
+  if (sizeof(typename IO::type) == 2) {
+    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(g, -1.44269504f, -16.0f));
+    return g * (__builtin_amdgcn_rcpf(0x1p-16f + e) * 0x1p-16f);
+  }
+  if (g < -60.0f) {
+    const float h = expf(0.5f * g);
+    return g * h * h;
+  }
   return g / (1.0f + expf(-g));
 }
 

@@ -160,3 +160,40 @@ def test_route_backward_shows_nan(score, renorm, E, K):
                 want[r, named] = bad[named]
         assert torch.equal(torch.isnan(dx), want), (dtype, torch.isnan(dx).sum(1), want.sum(1))
         assert (dx[5] == 0).all()
+
+
+# -------------------------------------------------------------------------------- products
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("M,width", [(5, 64), (40, 64), (300, 4096 + 9), (600, 16385)])  # split, 128 and 256 rows a tile
+def test_gates_that_close_and_open(dtype, M, width):
+    """silu of gates down to where exp(gate) leaves fp32, times large ups: relative to the value as
+    elsewhere.  The product's values are exact here (codes of one, scales of powers of two and gates
+    themselves).  What silu itself has below the normal range is lost by half a step of fp32's smallest
+    values, and for 16-bit results by scores below 2^-142, which count as 0."""
+    t = DTYPES[dtype]
+    K = 16
+    gates = torch.cat([torch.linspace(-150, -75, M - M // 2, device=DEV), torch.linspace(-75, 200, M // 2, device=DEV)])
+    a = torch.zeros(M, K, dtype=torch.int8, device=DEV)
+    a[:, 0] = 1
+    w = torch.zeros(2 * width, K, dtype=torch.int8, device=DEV)
+    w[:, 0] = 1
+    ups = 2.0 ** (torch.arange(width, device=DEV) % 5 * 25 - 10.0)  # 2^-10 .. 2^90
+    sw = torch.cat([torch.ones(width, device=DEV), ups])
+    got = ep.matmul_int8((a, gates.contiguous()), (w, sw), gated=True, out_dtype=t).double()
+    g = gates.double()[:, None]
+    up = g * ups.double()[None, :]
+    ref = g / (1 + torch.exp(-g)) * up
+    rel = (4 * (1 + g.abs()) + 16) * U
+    lost = 2.0 ** -149 if t == torch.float32 else 2.0 ** -142 * g.abs()
+    # subnormal results: the last products lie on multiples of 2^-149, and bf16's subnormals are the multiples
+    # of 2^-126 / 2^7 = 2^-133, fp16's of 2^-14 / 2^10 = 2^-24: a rounding to them is off by half of that
+    step = {torch.float32: 2.0 ** -148, torch.bfloat16: 2.0 ** -134 + 2.0 ** -148, torch.float16: 2.0 ** -25}[t]
+    tol = ref.abs() * (rel + half_step(t) * (1 + rel)) + lost * up.abs() + step
+    if t == torch.float16:                            # beyond its largest value
+        big = ref.abs() * (1 + rel) >= 65504
+        assert (got.abs() >= 65504 * (1 - 2 * half_step(t)))[big].all()
+        got, ref = torch.where(big, 0.0, got), torch.where(big, 0.0, ref)
+    over = (got - ref).abs() - tol
+    at = int(over.argmax())
+    assert over.max() <= 0, (float(gates[at // width]), float(ups[at % width]), float(got.flatten()[at]), float(ref.flatten()[at]))
