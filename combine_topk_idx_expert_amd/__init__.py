@@ -34,6 +34,7 @@ from ._native import (  # noqa: F401
     comm_stream,
     debug_copy,
     debug_e4m3_encode,
+    debug_matmul_kernels,
     dispatch,
     dispatch_cached,
     expert_rows,

@@ -9,7 +9,7 @@ import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libep_mi355x.so"
-EP_ABI_VERSION = 5
+EP_ABI_VERSION = 6
 
 # dispatch flags
 _FP8 = 1
@@ -21,6 +21,8 @@ _SYMMETRIC_WINDOWS = 1
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
 _GATED = 1
+# EP_KERNEL_* bits
+_KERNELS = {1: "split", 2: "tiles128", 4: "tiles256"}
 # ep_handle_status bits
 STATUS_ROUTING = 1
 STATUS_TRUNCATED = 2
@@ -206,6 +208,8 @@ def lib() -> ctypes.CDLL:
         L.ep_debug_timing.restype = i32
         L.ep_debug_copy.argtypes = [vp, vp, i64, vp]
         L.ep_debug_copy.restype = i32
+        L.ep_debug_matmul_kernels.argtypes = [i64, i32, i32, u32, ctypes.POINTER(u32)]
+        L.ep_debug_matmul_kernels.restype = i32
         L.ep_last_error.argtypes = []
         L.ep_last_error.restype = ctypes.c_char_p
         L.ep_abi_version.argtypes = []
@@ -798,6 +802,14 @@ def debug_e4m3_encode(q):
     out = torch.empty(q.shape, dtype=torch.uint8, device=q.device)
     _check(lib().ep_debug_e4m3_encode(_ptr(q), _ptr(out), q.numel(), _stream(q.device)))
     return out
+
+
+def debug_matmul_kernels(num_rows: int, num_groups: int, outer: int, gated: bool = False) -> tuple:
+    """Names of the kernels that matmul_int8 launches for these sizes (num_groups 0: dense), by
+    ep_debug_matmul_kernels: "split", "tiles128", "tiles256".  Host only."""
+    bits = ctypes.c_uint32()
+    _check(lib().ep_debug_matmul_kernels(num_rows, num_groups, outer, _GATED if gated else 0, ctypes.byref(bits)))
+    return tuple(name for bit, name in _KERNELS.items() if bits.value & bit)
 
 
 def debug_copy(dst, src):

@@ -764,18 +764,13 @@ ep_status ep_matmul_int8(const int8_t* a, const float* a_scale, int64_t num_rows
                          const float* w_scale, int32_t num_groups, const int64_t* row_start,
                          const int32_t* row_count, int32_t inner, int32_t outer, uint32_t flags, int32_t out_type,
                          void* out, void* stream) {
-  if (flags & ~(uint32_t)EP_MATMUL_GATED) return fail(EP_ERR_SHAPE, "unknown matmul flags 0x%x", flags);
+  const ep_status st = validate_matmul(num_rows, num_groups, outer, flags);
+  if (st != EP_OK) return st;
   if (out_type != EP_TYPE_F32 && out_type != EP_TYPE_BF16 && out_type != EP_TYPE_F16)
     return fail(EP_ERR_SHAPE, "unknown element type %d", out_type);
   const bool gated = flags & EP_MATMUL_GATED;
-  if (num_rows < 0 || num_groups < 0 || num_groups > EP_MAX_EXPERTS)
-    return fail(EP_ERR_SHAPE, "bad sizes: %lld rows, %d groups (at most %d)", (long long)num_rows, num_groups,
-                EP_MAX_EXPERTS);
   if (inner < 16 || inner % 16 != 0 || inner > EP_MAX_MATMUL_INNER)
     return fail(EP_ERR_SHAPE, "inner %d must be a multiple of 16 in [16, %d]", inner, EP_MAX_MATMUL_INNER);
-  if (outer < 1 || outer > EP_MAX_MATMUL_OUTER || (gated && outer % 2 != 0))
-    return fail(EP_ERR_SHAPE, "outer %d must lie in [1, %d] and be even for a gated product", outer, EP_MAX_MATMUL_OUTER);
-  if (num_rows >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "num_rows %lld reaches 2^31", (long long)num_rows);
   if (num_rows == 0) return EP_OK;
   if (!a || !a_scale || !w || !w_scale || !out) return fail(EP_ERR_NULL, "a / a_scale / w / w_scale / out is NULL");
   if (num_groups > 0 && (!row_start || !row_count)) return fail(EP_ERR_NULL, "row_start / row_count is NULL");
@@ -895,6 +890,16 @@ ep_status ep_debug_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* s
   if ((threads + 255) / 256 >= ((int64_t)1 << 31)) return fail(EP_ERR_OVERFLOW, "n too large");
   e4m3_encode_kernel<<<(int)((threads + 255) / 256), 256, 0, (hipStream_t)stream>>>(in, out, n);
   EP_LAUNCHED("e4m3_encode_kernel");
+  return EP_OK;
+}
+
+ep_status ep_debug_matmul_kernels(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags,
+                                  uint32_t* kernels) {
+  if (!kernels) return fail(EP_ERR_NULL, "kernels is NULL");
+  const ep_status st = validate_matmul(num_rows, num_groups, outer, flags);
+  if (st != EP_OK) return st;
+  const bool gated = flags & EP_MATMUL_GATED;
+  *kernels = num_rows == 0 ? 0 : matmul_kernels(num_rows, num_groups, gated ? outer / 2 : outer, gated);
   return EP_OK;
 }
 

@@ -20,6 +20,17 @@ ep_status with_type(int32_t type, F f) {
 
 uintptr_t type_bytes(int32_t type) { return type == EP_TYPE_F32 ? 4 : 2; }
 
+ep_status validate_matmul(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags) {
+  if (flags & ~(uint32_t)EP_MATMUL_GATED) return fail(EP_ERR_SHAPE, "unknown matmul flags 0x%x", flags);
+  if (num_rows < 0 || num_groups < 0 || num_groups > EP_MAX_EXPERTS)
+    return fail(EP_ERR_SHAPE, "bad sizes: %lld rows, %d groups (at most %d)", (long long)num_rows, num_groups,
+                EP_MAX_EXPERTS);
+  if (outer < 1 || outer > EP_MAX_MATMUL_OUTER || ((flags & EP_MATMUL_GATED) && outer % 2 != 0))
+    return fail(EP_ERR_SHAPE, "outer %d must lie in [1, %d] and be even for a gated product", outer, EP_MAX_MATMUL_OUTER);
+  if (num_rows >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "num_rows %lld reaches 2^31", (long long)num_rows);
+  return EP_OK;
+}
+
 ep_status validate_route(const ep_route_config* c, int32_t type, int64_t num_tokens, int64_t row_stride) {
   if (!c) return fail(EP_ERR_NULL, "route config is NULL");
   if (c->num_experts < 1 || c->num_experts > EP_MAX_EXPERTS)
@@ -241,29 +252,35 @@ ep_status launch_matmul_few(const MatmulArgs& a, hipStream_t s) {
   }
 }
 
+// EP_KERNEL_* of the launches for M rows in G groups (0: dense) and `width` columns of out.
+uint32_t matmul_kernels(int64_t M, int G, int width, bool gated) {
+  const int bc = gated ? 128 : 256;
+  const int64_t n_tiles = (width + bc - 1) / bc;
+  if (G == 0) {
+    if ((M + 255) / 256 * n_tiles >= 3 * kCUs / 4) return EP_KERNEL_TILES_256;
+    if (M > kFewRows && (M + 127) / 128 * n_tiles >= 3 * kCUs / 8) return EP_KERNEL_TILES_128;
+    return EP_KERNEL_SPLIT;
+  }
+  const int64_t mean = M / G;
+  // row tiles that large groups can fill: a tile has more than kFewRows rows
+  const int64_t large = std::min(M / 256 + G, M / (kFewRows + 1));
+  if (large * n_tiles < (mean <= 2 * kFewRows ? kCUs / 2 + 1 : 3 * kCUs / 8)) return EP_KERNEL_SPLIT;
+  return ((M / 256 + G) * n_tiles >= 3 * kCUs / 4 ? EP_KERNEL_TILES_256 : EP_KERNEL_TILES_128) |
+         (mean < 4 * kFewRows ? EP_KERNEL_SPLIT : 0);
+}
+
 template <typename IO, bool GATED>
 ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
-  const int bc = GATED ? 128 : 256;
-  const int64_t n_tiles = (a.width + bc - 1) / bc;
+  const uint32_t kernels = matmul_kernels(a.M, a.row_start ? a.G : 0, a.width, GATED);
   a.least = 0;
   a.most = a.M;
-  if (!a.row_start) {
-    if ((a.M + 255) / 256 * n_tiles >= 3 * kCUs / 4) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
-    if (a.M > kFewRows && (a.M + 127) / 128 * n_tiles >= 3 * kCUs / 8)
-      return launch_matmul_tile<IO, GATED, 128, 256, 2, 4, false>(a, s);
-    return launch_matmul_few<IO, GATED>(a, s);
-  }
-  const int64_t mean = a.M / a.G;
-  // row tiles that large groups can fill: a tile has more than kFewRows rows
-  const int64_t large = std::min(a.M / 256 + a.G, a.M / (kFewRows + 1));
-  if (large * n_tiles < (mean <= 2 * kFewRows ? kCUs / 2 + 1 : 3 * kCUs / 8)) return launch_matmul_few<IO, GATED>(a, s);
-  if (mean < 4 * kFewRows) {
+  if (kernels & EP_KERNEL_SPLIT) {
     MatmulArgs few = a;
-    few.most = kFewRows;
+    if (kernels != EP_KERNEL_SPLIT) few.most = kFewRows;
     const ep_status st = launch_matmul_few<IO, GATED>(few, s);
-    if (st != EP_OK) return st;
+    if (st != EP_OK || kernels == EP_KERNEL_SPLIT) return st;
     a.least = kFewRows + 1;
   }
-  if ((a.M / 256 + a.G) * n_tiles >= 3 * kCUs / 4) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
+  if (kernels & EP_KERNEL_TILES_256) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
   return launch_matmul_tile<IO, GATED, 128, 256, 2, 4, false>(a, s);
 }

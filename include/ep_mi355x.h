@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define EP_ABI_VERSION 5
+#define EP_ABI_VERSION 6
 
 /* Limits of the library. */
 #define EP_MAX_RANKS 1024
@@ -507,6 +507,16 @@ ep_status ep_debug_e4m3_encode(const float *in, uint8_t *out, int64_t n, void *s
  * combine kernels.  Async on `stream`; gives the copy ceiling their bandwidth
  * is compared with.  Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
 ep_status ep_debug_copy(void *dst, const void *src, int64_t nbytes, void *stream);
+
+/* Test hook, not part of the method: which kernels ep_matmul_int8 launches for these sizes
+ * (EP_KERNEL_* bits; 0 for no rows), so that a test can name the kernel it is about.  With
+ * more than one, groups of at most 64 rows are the split's.  Host only.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW. */
+#define EP_KERNEL_SPLIT 1u     /* few rows, split over the inner size */
+#define EP_KERNEL_TILES_128 2u /* tiles of 128 rows                   */
+#define EP_KERNEL_TILES_256 4u /* tiles of 256 rows                   */
+ep_status ep_debug_matmul_kernels(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags,
+                                  uint32_t *kernels);
 
 /* Profiling hook, not part of the method: the device-side timing slots of a
  * library built with EP_DEVICE_TIMING=1 ("Ascend DeepEP MoE Dispatch
