@@ -350,7 +350,12 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // Scores are not: a row where two neighbours among the choices, the last choice
 // and the best expert left out, or a kept and a dropped group, lie within the
 // error of the fp32 scores (and are not equal for being made of equal numbers)
-// is done over in 64 bits by the whole wave (route_row), about one row in 500.
+// is done over in 64 bits by the whole wave (route_row), rows of masked tokens too.
+// How many that are depends on the data, since the margins do not shrink with small
+// scores.  Top 8 of 256: one row in 800 to 1100 for normal logits of deviation 1.5; one in
+// 22 for sigmoids of deviation 5 under a bias of deviation 0.001; one in 8 for softmax of
+// deviation 5 under a bias of 0.0008; nearly all for saturated sigmoids (deviation 8)
+// without a bias but with sums of two.
 //
 // Vector instructions bound it, ~165 a row of 256 with groups and bias: 262144 rows
 // of fp32 in 92 us, 60% of the memory's rate; 32768 rows of bf16 by logits 9-10 us; one
@@ -611,6 +616,8 @@ __global__ __launch_bounds__(kWave) void route_lanes_kernel(RouteArgs a, RouteLa
       for (int i = 0; i < VPL; ++i) key[i] = i < have ? key[i] : kNegInf;
     }
     if (a.bias) {
+      // rounded score plus bias in every branch: keys of equal parts tie wherever their bias is read
+#pragma clang fp contract(off)
       float best = kNegInf, worst = 0.0f;
       if (p.bias_vec) {
 #pragma unroll
@@ -926,6 +933,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
 // 25; dense, 131072 x 256 bf16 in 33 us, 4.3 TB/s (one row a wave: 189 and 179 us).
 // NCH > 0: the dense form with a lane's NCH pieces of the row in registers, read
 // and raised once; 0: every other case (vec: dense rows of whole pieces).
+// The rows in registers are raised by the hardware's exp2 (fast_exp): a score d below
+// the row's largest is off by 3 u d relative, u = 2^-24 (the difference, the factor
+// log2 e, their product), one by expf by u d, and is 0 below the normal range.  d exp(-d)
+// < 0.37, so that this adds 0.8 u of the largest score to an error of several u.
 template <typename IO, int LPR, int NCH>
 __global__ __launch_bounds__(kWave) void route_backward_lanes_kernel(RouteBwdArgs a, int vec) {
   constexpr int kRows = kWave / LPR;

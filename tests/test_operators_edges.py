@@ -83,6 +83,30 @@ def test_route_groups_whose_sum_leaves_fp32(score, E, K, groups, kept):
         check_ids(rc, x, bias)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,groups,kept,group_score", [
+    (61, 8, 1, 1, "max"), (62, 8, 1, 1, "max"), (63, 16, 1, 1, "max"), (250, 8, 1, 1, "max"), (253, 13, 1, 1, "max"),
+    (255, 8, 3, 2, "top2"), (54, 11, 6, 3, "top2"), (500, 9, 1, 1, "max"), (497, 8, 7, 3, "max")])
+def test_route_ties_under_a_bias_at_the_end_of_a_row(score, E, K, groups, kept, group_score):
+    """Few logits, few biases that are no sums of powers of two: keys of equal parts tie, wherever the
+    bias was read."""
+    g = generator(E)
+    rc = ep.RouteConfig(E=E, K=K, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
+    store = torch.empty(E + 4, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randint(-2, 3, (300, E), generator=g, device=DEV).to(dtype)
+        x[0] = 0.0
+        x[1, : E - 3] = -1.0
+        x[2, ::2] = -INF
+        for values in ([0.1], [0.3, 0.7], [-0.3, 0.1, 1.1]):
+            v = torch.tensor(values, device=DEV)
+            b = v[torch.randint(0, len(values), (E,), generator=g, device=DEV)]
+            for off in (0, 1):                        # a bias that is not 16-byte aligned
+                bias = store[off:off + E]
+                bias.copy_(b)
+                check_ids(rc, x, bias)
+
+
 # ------------------------------------------------------------------- gradient of the router
 
 GRADIENTS = [(64, 4), (61, 5), (256, 8), (600, 6), (256, 12), (256, 20), (1030, 5)]
@@ -160,6 +184,29 @@ def test_route_backward_shows_nan(score, renorm, E, K):
                 want[r, named] = bad[named]
         assert torch.equal(torch.isnan(dx), want), (dtype, torch.isnan(dx).sum(1), want.sum(1))
         assert (dx[5] == 0).all()
+
+
+@pytest.mark.parametrize("E", [64, 61, 250, 1024, 1030])
+def test_route_backward_dense_of_distant_logits(E):
+    """Softmax over all experts in fp32, scores far below the row's largest: the exponential's argument is
+    off by 3 u for each unit of the distance (the difference, the factor log2 e, their product), the
+    exponential, the sum and the products by some roundings; scores below the normal range are 0."""
+    g = generator(E)
+    K = 4
+    x = torch.randn(64, E, generator=g, device=DEV) * 20
+    rc = ep.RouteConfig(E=E, K=K, renormalize=False)
+    idx, _ = ep.route(rc, x)
+    gw = torch.rand(64, K, generator=g, device=DEV) + 0.5
+    got = f64(ep.route_backward(rc, x, idx, gw))
+    ref = plain.route_backward(rc, f64(x), idx.cpu().numpy(), f64(gw))
+    rest = np.ones((64, E), bool)
+    np.put_along_axis(rest, idx.cpu().numpy(), False, 1)
+    # unchosen: -p sum(g p); the sum is off by what its largest scores are, whose distances are small or
+    # whose part is (d exp(-d) < 0.37 for each of them)
+    far = f64(x).max(1, keepdims=True) - f64(x)
+    tol = np.abs(ref) * (3 * far + E / 8 + 40) * U + 2.0 ** -126 * 2
+    over = np.where(rest, np.abs(got - ref) - tol, -1)
+    assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
 
 
 # -------------------------------------------------------------------------------- products
