@@ -200,15 +200,21 @@ ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
 //  - tiles of 256 x 256 once they fill three quarters of the CUs; below that
 //    tiles of 128 x 256 while they fill three eighths (2048 x 7168 x 4096 gated: 67
 //    against 82 us; 8192 x 8192 x 8192: 256 x 256 by 10%);
-//  - below that, or for at most 64 rows, the split over the inner size (512 x 7168
-//    x 4096 gated: 23 us against 54 and 79; 64 rows: 9 against 44 and 49).
+//  - below that, and for at most 64 rows whatever the width, the split over the inner
+//    size (512 x 7168 x 4096 gated: 23 us against 54 and 79; 64 rows: 9 against 44 and
+//    49; 1 x 7168 x 49152: 63 against 88 and 90, 64 rows of it 87 against 91 and 93).
 // Groups: their sizes are on the device.  A group of at most kFewRows rows is
 // the split's and a larger one the tiles'; each launch passes over the others'
-// groups.  No second launch where large groups cannot fill half of the tiles' grid
-// (8 groups of 72 rows, 7168 x 4096 gated: 72 us by the split alone, 84 by both), or
-// three eighths for tall groups, whose rows the split takes 64 at a time (8 of 1696,
+// groups.  No second launch where large groups cannot fill more than half of the tiles'
+// grid (8 groups of 72 rows, 7168 x 4096 gated: 72 us by the split alone, 84 by both),
+// or three eighths for tall groups, whose rows the split takes 64 at a time (8 of 1696,
 // 4672 x 318 gated: 46 us by tiles, 80 by the split); nor a first one where the mean
-// is so large that few groups are small.
+// is so large that few groups are small.  129 random shapes (2 to 64 groups, inner 320
+// to 7168): with 96 to 128 tiles of large groups, tiles take 1.28 times the split's time
+// for means of up to 128 rows, 1.03 for 129 to 199, 0.72 above; with fewer 1.22, 1.22 and
+// 0.97, with up to 192 1.00, 0.85 and 0.72.  The rule is within 10% of the fastest of the
+// three in 106 of them and 4% off on average (at worst 1.6 times: 32 groups of 112
+// rows, 2048 x 256, by the split 35 us, by tiles 22).
 constexpr int64_t kFewRows = 64;
 
 // The split's tile, MT x NT sixteens of rows and channels.  Its time is that of the
@@ -257,14 +263,15 @@ uint32_t matmul_kernels(int64_t M, int G, int width, bool gated) {
   const int bc = gated ? 128 : 256;
   const int64_t n_tiles = (width + bc - 1) / bc;
   if (G == 0) {
+    if (M <= kFewRows) return EP_KERNEL_SPLIT;
     if ((M + 255) / 256 * n_tiles >= 3 * kCUs / 4) return EP_KERNEL_TILES_256;
-    if (M > kFewRows && (M + 127) / 128 * n_tiles >= 3 * kCUs / 8) return EP_KERNEL_TILES_128;
+    if ((M + 127) / 128 * n_tiles >= 3 * kCUs / 8) return EP_KERNEL_TILES_128;
     return EP_KERNEL_SPLIT;
   }
   const int64_t mean = M / G;
   // row tiles that large groups can fill: a tile has more than kFewRows rows
   const int64_t large = std::min(M / 256 + G, M / (kFewRows + 1));
-  if (large * n_tiles < (mean <= 2 * kFewRows ? kCUs / 2 + 1 : 3 * kCUs / 8)) return EP_KERNEL_SPLIT;
+  if (mean <= 2 * kFewRows ? large * n_tiles <= kCUs / 2 : large * n_tiles < 3 * kCUs / 8) return EP_KERNEL_SPLIT;
   return ((M / 256 + G) * n_tiles >= 3 * kCUs / 4 ? EP_KERNEL_TILES_256 : EP_KERNEL_TILES_128) |
          (mean < 4 * kFewRows ? EP_KERNEL_SPLIT : 0);
 }

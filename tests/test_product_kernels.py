@@ -32,6 +32,9 @@ def gpu():
 def test_kernels_are_named_for_sizes():
     assert ep.debug_matmul_kernels(0, 0, 64) == ()
     assert ep.debug_matmul_kernels(1, 0, 4096, gated=True) == ("split",)
+    for rows in (1, 64):  # few rows, however wide
+        assert ep.debug_matmul_kernels(rows, 0, 1 << 20) == ep.debug_matmul_kernels(rows, 0, 1 << 20, True) == ("split",)
+    assert ep.debug_matmul_kernels(65, 0, 49152) == ("tiles256",)
     assert ep.debug_matmul_kernels(8192, 0, 8192) == ("tiles256",)
     assert ep.debug_matmul_kernels(1003, 0, 7168) == ("tiles128",)
     assert ep.debug_matmul_kernels(96, 32, 4096, gated=True) == ("split",)
@@ -122,7 +125,7 @@ DENSE = [
     (T128, 300, 256, 8192, 4096), (T128, 129, 400, 12037, 6021), (T128, 1003, 2048, 7168, 2000), (T128, 1025, 144, 3000, 1500),
     (T128, 641, 16, 4100, 2050), (T128, 300, 1040, 8195, 4101), (T128, 127, 80, 24577, 12300),
     (T256, 300, 1040, 24577, 12289), (T256, 2100, 256, 5637, 2821), (T256, 4096 + 1, 656, 3000, 1500),
-    (T256, 4096 + 129, 2064, 2817, 1409), (T256, 1, 160, 49151, 24577), (T256, 513, 16, 16300, 8200),
+    (T256, 4096 + 129, 2064, 2817, 1409), (T256, 65, 160, 49151, 24577), (T256, 513, 16, 16300, 8200),
     (T256, 6000, 7168, 2100, 1100), (T256, 1025, 80, 10000, 4993),
 ]
 
