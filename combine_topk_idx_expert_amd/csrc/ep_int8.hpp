@@ -252,7 +252,7 @@ __device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int 
 // keeps many loads in flight.  A workgroup has 16 * MT rows by NT channel tiles
 // of 16; the KW waves join their sums, which are whole numbers and do not depend
 // on the split, through LDS.  Bound by the memory where weights are many (32 groups
-// of 3 rows, 7168 x 4096 gated: 151 us, 6.2 TB/s of weights), else by the loads of
+// of 3 rows, 7168 x 4096 gated: 149 us, 6.3 TB/s of weights), else by the loads of
 // the CU with the most workgroups, ~24 bytes a clock (one row: 7.4 us).
 //
 // A wave has a ring of S stages of LDS to itself and no barrier before the end:

@@ -21,11 +21,11 @@ namespace ep {
 // barrier, and the next tile's first steps arrive during a tile's epilogue.
 //
 // What bounds it: a step takes 1470 cycles (256 x 256; 990 at 128 x 256) against 1024
-// (512) of products.  The direct loads alone come at ~24 bytes a clock and CU, the
-// L1's outstanding requests over their latency, so more stages change nothing; and
+// (512) of products.  The direct loads alone come at ~24 bytes a clock and CU (a
+// probe of them from the L2: 42 to 54), and more stages change nothing; and
 // under int8 products the clock falls to 1.7-1.9 GHz of 2.4.  65536 rows of 64 groups,
-// 7168 x 4096 gated: 1771 us, 2.17e15 operations a second; 16384 rows, 2048 x 7168:
-// 340 us; 1003 x 2048 x 7168 (128 x 256): 22 us.
+// 7168 x 4096 gated: 1775 us, 2.17e15 operations a second; 16384 rows, 2048 x 7168:
+// 341 us; 1003 x 2048 x 7168 (128 x 256): 22 us.
 //
 // LDS image of a stage: 64 bytes a row, its four 16-byte chunks in the order
 // chunk ^ order(row / 4 % 4), so that the lanes that ds_read_b128 serves

@@ -357,8 +357,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
 // deviation 5 under a bias of 0.0008; nearly all for saturated sigmoids (deviation 8)
 // without a bias but with sums of two.
 //
-// Vector instructions bound it, ~165 a row of 256 with groups and bias: 262144 rows
-// of fp32 in 92 us, 60% of the memory's rate; 32768 rows of bf16 by logits 9-10 us; one
+// Vector instructions bound it, 180 a row of 256 with groups and bias: 262144 rows
+// of fp32 in 92 us, 3.2 TB/s; 32768 rows of bf16 by logits 9-10 us; one
 // row 5.3 us, a wave's latency.  One row a wave in 64 bits took 759 and 38 us.
 
 // Over the N (8 or 16) lanes of a row; every lane gets the result.
