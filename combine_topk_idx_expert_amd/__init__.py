@@ -42,7 +42,10 @@ from ._native import (  # noqa: F401
     lib,
     lib_path,
     matmul_int8,
+    quantize_fp8,
     quantize_int8,
+    rms_norm,
+    rms_norm_backward,
     relayout,
     route,
     route_backward,

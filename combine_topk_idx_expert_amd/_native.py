@@ -9,7 +9,7 @@ import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libep_mi355x.so"
-EP_ABI_VERSION = 6
+EP_ABI_VERSION = 7
 
 # dispatch flags
 _FP8 = 1
@@ -21,6 +21,8 @@ _SYMMETRIC_WINDOWS = 1
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
 _GATED = 1
+# scales of E4M3 rows by columns (ep_quantize_fp8, ep_matmul_fp8)
+_FP8_COL_MAJOR = 2
 # EP_KERNEL_* bits
 _KERNELS = {1: "split", 2: "tiles128", 4: "tiles256"}
 # ep_handle_status bits
@@ -201,6 +203,13 @@ def lib() -> ctypes.CDLL:
         L.ep_expert_rows.argtypes = [vp, vp, vp, vp]
         L.ep_matmul_int8.argtypes = [vp, vp, i64, vp, vp, i32, vp, vp, i32, i32, u32, i32, vp, vp]
         for fn in ("ep_route", "ep_route_backward", "ep_quantize_int8", "ep_expert_rows", "ep_matmul_int8"):
+            getattr(L, fn).restype = i32
+        f32 = ctypes.c_float
+        L.ep_quantize_fp8.argtypes = [i32, vp, i64, i32, i64, u32, vp, vp, vp]
+        L.ep_rms_norm.argtypes = [i32, vp, i64, vp, i64, vp, i32, f32, i64, i32, vp, vp, vp, vp, vp]
+        L.ep_rms_norm_backward_workspace.argtypes = [i32, i64, i32, ctypes.POINTER(i64)]
+        L.ep_rms_norm_backward.argtypes = [i32, vp, i64, vp, i32, f32, vp, i64, vp, i64, i64, i32, vp, vp, vp, vp]
+        for fn in ("ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
             getattr(L, fn).restype = i32
         L.ep_debug_e4m3_encode.argtypes = [vp, vp, i64, vp]
         L.ep_debug_e4m3_encode.restype = i32
@@ -791,6 +800,128 @@ def matmul_int8(a, w, rows=None, gated: bool = False, out_dtype=None, out=None):
     _launch(device, lib().ep_matmul_int8, x.data_ptr(), xs.data_ptr(), M, wc.data_ptr(), wsc.data_ptr(), G,
             _ptr(start), _ptr(count), K, N, _GATED if gated else 0, code, out.data_ptr())
     return out
+
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 channels."""
+    return (n + 127) // 128
+
+
+def quantize_fp8(x, scales_col_major: bool = False, out=None):
+    """ep_quantize_fp8: x [N, H] (float32, bfloat16 or float16, rows may be apart) -> (codes uint8
+    [N, H], scales float32 [N, ceil(H / 128)], or [ceil(H / 128), N] with scales_col_major): the
+    codes that dispatch(fp8=True) makes.  out: optional (codes, scales)."""
+    import torch
+
+    code, N, H, stride, device = _require_rows(x, "x")
+    nb = _blocks(H)
+    shape = (nb, N) if scales_col_major else (N, nb)
+    if out is None:
+        codes = torch.empty_strided((N, H), (H, 1), dtype=torch.uint8, device=device)
+        scales = torch.empty_strided(shape, (shape[1], 1), dtype=torch.float32, device=device)
+    else:
+        codes, scales = out
+        _require(codes, torch.uint8, (N, H), "codes", device)
+        _require(scales, torch.float32, shape, "scales", device)
+    _launch(device, lib().ep_quantize_fp8, code, x.data_ptr(), N, H, stride, _FP8_COL_MAJOR if scales_col_major else 0,
+            codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def _norm_weight(weight, code, H, device):
+    """EP_TYPE_* of a norm's weight [H], which has the rows' type or float32."""
+    import torch
+
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    wcode = _type(weight.dtype, "weight")
+    if wcode != code and wcode != 0:
+        raise TypeError(f"weight must have the rows' type or be float32, got {weight.dtype}")
+    _require(weight, weight.dtype, (H,), "weight", device)
+    return wcode
+
+
+def _same_rows(t, name, code, N, H, device):
+    """Row stride of a matrix that has to match the rows' type, shape and device."""
+    tcode, n, _, stride, dev = _require_rows(t, name, H)
+    if tcode != code:
+        raise TypeError(f"{name} must have the rows' type, got {t.dtype}")
+    if n != N:
+        raise ValueError(f"{name} must have {N} rows, got {n}")
+    if dev != device:
+        raise ValueError(f"{name} is on {dev}, the rows on {device}")
+    return stride
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, fp8: bool = False, keep: bool = True, out=None):
+    """ep_rms_norm: x [N, H] (float32, bfloat16 or float16, rows may be apart) -> (y, quantized, total).
+
+    y: the norm of x + residual times weight ([H], x's type or float32), in x's type; None with
+    fp8=True, keep=False.  quantized: with fp8 the pair (codes uint8 [N, H], scales float32 [N,
+    ceil(H / 128)]) of the norm, as dispatch takes it; else None.  total: x + residual in x's type;
+    None without a residual.  out: optional tuple of the same three; total may be x or residual
+    themselves (the sum in place)."""
+    import torch
+
+    code, N, H, stride, device = _require_rows(x, "x")
+    wcode = _norm_weight(weight, code, H, device)
+    rstride = 0 if residual is None else _same_rows(residual, "residual", code, N, H, device)
+    if not (fp8 or keep):
+        raise ValueError("keep=False needs fp8=True: nothing would be written")
+    y = total = codes = scales = None
+    if out is None:
+        if keep:
+            y = torch.empty_strided((N, H), (H, 1), dtype=x.dtype, device=device)
+        if fp8:
+            nb = _blocks(H)
+            codes = torch.empty_strided((N, H), (H, 1), dtype=torch.uint8, device=device)
+            scales = torch.empty_strided((N, nb), (nb, 1), dtype=torch.float32, device=device)
+        if residual is not None:
+            total = torch.empty_strided((N, H), (H, 1), dtype=x.dtype, device=device)
+    else:
+        if not (isinstance(out, tuple) and len(out) == 3):
+            raise TypeError("out must be a tuple (y, quantized, total)")
+        if keep:
+            y = out[0]
+            _require(y, x.dtype, (N, H), "y", device)
+        if fp8:
+            codes, scales = out[1]
+            _require(codes, torch.uint8, (N, H), "codes", device)
+            _require(scales, torch.float32, (N, _blocks(H)), "scales", device)
+        if residual is not None:
+            total = out[2]
+            _require(total, x.dtype, (N, H), "total", device)
+    _launch(device, lib().ep_rms_norm, code, x.data_ptr(), stride, _ptr(residual), rstride, weight.data_ptr(), wcode, eps,
+            N, H, _ptr(total), _ptr(y), _ptr(codes), _ptr(scales))
+    return y, (codes, scales) if fp8 else None, total
+
+
+def rms_norm_backward(x, weight, grad, eps: float = 1e-6, grad_total=None, out=None):
+    """ep_rms_norm_backward -> (grad_x [N, H] in x's type, grad_weight float32 [H]).
+
+    x: what was normalised (total where a residual was added; grad_x is then the gradient of both).
+    grad: the gradient of y; grad_total: optional gradient that reaches total past the norm, added
+    to grad_x.  Rows may be apart.  out: optional (grad_x, grad_weight); grad_x may be grad or
+    grad_total themselves."""
+    import torch
+
+    code, N, H, stride, device = _require_rows(x, "x")
+    wcode = _norm_weight(weight, code, H, device)
+    gstride = _same_rows(grad, "grad", code, N, H, device)
+    tstride = 0 if grad_total is None else _same_rows(grad_total, "grad_total", code, N, H, device)
+    if out is None:
+        gx = torch.empty_strided((N, H), (H, 1), dtype=x.dtype, device=device)
+        gw = torch.empty_strided((H,), (1,), dtype=torch.float32, device=device)
+    else:
+        gx, gw = out
+        _require(gx, x.dtype, (N, H), "grad_x", device)
+        _require(gw, torch.float32, (H,), "grad_weight", device)
+    size = ctypes.c_int64()
+    _check(lib().ep_rms_norm_backward_workspace(code, N, H, ctypes.byref(size)))
+    space = torch.empty(size.value, dtype=torch.uint8, device=device)
+    _launch(device, lib().ep_rms_norm_backward, code, x.data_ptr(), stride, weight.data_ptr(), wcode, eps, grad.data_ptr(),
+            gstride, _ptr(grad_total), tstride, N, H, gx.data_ptr(), gw.data_ptr(), space.data_ptr())
+    return gx, gw
 
 
 def debug_e4m3_encode(q):

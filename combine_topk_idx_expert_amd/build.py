@@ -2,13 +2,15 @@
 
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "ep_api.hip")
+SRC = [os.path.join(PKG, "csrc", f) for f in ("ep_api.hip", "ep_norm.hip")]
 LIB = os.path.join(PKG, "libep_mi355x.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -17,7 +19,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # no packed fp32 instructions in any kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
@@ -30,10 +31,7 @@ def sources() -> list[str]:
     return [os.path.join(d, f) for f in sorted(os.listdir(d))] + [os.path.join(ROOT, "include", "ep_mi355x.h")]
 
 
-def build(verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:
-    out = out or LIB
-    tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(extra or []), SRC, "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -44,6 +42,18 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str | None
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if msgs and verbose:
         print("\n".join(msgs), file=sys.stderr)
+
+
+def build(verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:
+    """Compiles every source side by side and links them."""
+    out = out or LIB
+    tmp = out + ".tmp"
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(f) + ".o") for f in SRC]
+        with concurrent.futures.ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda so: _run([HIPCC, *FLAGS, *(extra or []), "-c", so[0], "-o", so[1]], verbose),
+                          zip(SRC, objs)))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, out)
     return out
 

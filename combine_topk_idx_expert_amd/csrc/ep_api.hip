@@ -17,6 +17,7 @@
 
 #include "ep_mi355x.h"
 #include "ep_dispatch.hpp"
+#include "ep_host.hpp"
 #include "ep_int8.hpp"
 #include "ep_int8_tile.hpp"
 #include "ep_layout.hpp"
@@ -24,11 +25,9 @@
 
 using namespace ep;
 
-namespace {
+thread_local std::string ep::g_last_error;
 
-thread_local std::string g_last_error;
-
-ep_status fail(ep_status st, const char* fmt, ...) {
+ep_status ep::fail(ep_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -38,19 +37,7 @@ ep_status fail(ep_status st, const char* fmt, ...) {
   return st;
 }
 
-#define EP_HIP(call)                                                                      \
-  do {                                                                                    \
-    hipError_t e_ = (call);                                                               \
-    if (e_ != hipSuccess) return fail(EP_ERR_HIP, "%s: %s", #call, hipGetErrorString(e_)); \
-  } while (0)
-
-#define EP_LAUNCHED(name)                                                                     \
-  do {                                                                                        \
-    hipError_t e_ = hipGetLastError();                                                        \
-    if (e_ != hipSuccess) return fail(EP_ERR_HIP, "launch of %s: %s", name, hipGetErrorString(e_)); \
-  } while (0)
-
-bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+namespace {
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }

@@ -19,7 +19,7 @@ constexpr int kEpTimingPhases = 8;
 constexpr int kEpTimingGroups = 1024;
 enum { EP_TK_COUNT = 0, EP_TK_SCAN, EP_TK_FINALIZE, EP_TK_RANK, EP_TK_SMALL, EP_TK_DISPATCH, EP_TK_COMBINE };
 #if EP_DEVICE_TIMING
-__device__ uint64_t ep_timing_slots[kEpTimingKernels * kEpTimingPhases * kEpTimingGroups];
+static __device__ uint64_t ep_timing_slots[kEpTimingKernels * kEpTimingPhases * kEpTimingGroups];
 #define EP_TIMING_MARK(kernel, phase)                                                                    \
   do {                                                                                                   \
     if (threadIdx.x == 0 && blockIdx.x < (unsigned)kEpTimingGroups)                                      \

@@ -5,21 +5,6 @@
 // anonymous namespace, after the error helpers (fail, EP_LAUNCHED) it uses.
 #pragma once
 
-constexpr int kCUs = 256;  // MI355X
-
-// Calls f with the element-access type of an EP_TYPE_* value.
-template <typename F>
-ep_status with_type(int32_t type, F f) {
-  switch (type) {
-    case EP_TYPE_F32: return f(F32{});
-    case EP_TYPE_BF16: return f(Bf16{});
-    case EP_TYPE_F16: return f(F16{});
-    default: return fail(EP_ERR_SHAPE, "unknown element type %d", type);
-  }
-}
-
-uintptr_t type_bytes(int32_t type) { return type == EP_TYPE_F32 ? 4 : 2; }
-
 ep_status validate_matmul(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags) {
   if (flags & ~(uint32_t)EP_MATMUL_GATED) return fail(EP_ERR_SHAPE, "unknown matmul flags 0x%x", flags);
   if (num_rows < 0 || num_groups < 0 || num_groups > EP_MAX_EXPERTS)

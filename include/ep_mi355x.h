@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define EP_ABI_VERSION 6
+#define EP_ABI_VERSION 7
 
 /* Limits of the library. */
 #define EP_MAX_RANKS 1024
@@ -75,6 +75,7 @@ extern "C" {
 #define EP_MAX_QUANT_COLS (1 << 24)
 #define EP_MAX_MATMUL_INNER 131056 /* 128 * 128 * inner stays below 2^31 */
 #define EP_MAX_MATMUL_OUTER (1 << 20)
+#define EP_MAX_NORM_COLS 32768
 
 typedef enum {
   EP_OK = 0,
@@ -433,6 +434,76 @@ ep_status ep_matmul_int8(const int8_t *a, const float *a_scale, int64_t num_rows
                          const float *w_scale, int32_t num_groups, const int64_t *row_start,
                          const int32_t *row_count, int32_t inner, int32_t outer, uint32_t flags, int32_t out_type,
                          void *out, void *stream);
+
+/* --------------------------------------------------------------------------
+ * The expert layer in 8-bit floating point and in training: the norm in front
+ * of it, products of E4M3 rows (what ep_dispatch makes) and of 16-bit rows, and
+ * gradients.  As for the calls above: nothing is allocated, waited for or kept,
+ * all can be captured, the current device has to be the one that `stream` and
+ * the arrays belong to, and no output may overlap an input or another output
+ * where nothing else is said.
+ */
+
+/* With this flag the scales of E4M3 rows are [ceil(cols / 128), num_rows], one
+ * scale position contiguous across rows, as EP_DISPATCH_SCALES_COL_MAJOR makes
+ * them; without it [num_rows, ceil(cols / 128)]. */
+#define EP_FP8_SCALES_COL_MAJOR 2u
+
+/* ep_quantize_fp8 -- rows to E4M3FN codes with a scale for each 128 channels (the
+ * last block of a row is shorter where 128 does not divide num_cols).
+ *   x       device, [num_rows, num_cols] of `type`, rows row_stride elements apart.
+ *   codes   device, u8 [num_rows, num_cols] contiguous.
+ *   scales  device, fp32, see EP_FP8_SCALES_COL_MAJOR.
+ * scale = amax / 448 in fp32, code = E4M3FN round-to-nearest-even of the fp32
+ * quotient x / scale: the codes that ep_dispatch makes of bf16 rows.  A block of
+ * scale 0 (zeros, and an amax whose quotient is below fp32) has signed-zero codes;
+ * where the scale is subnormal, and so not amax / 448 to full precision, quotients
+ * are cut at 448.  A block holding NaN gets scale 0x7FC00000 and codes 0x7F, one
+ * holding infinities scale +Inf, codes 0x7F for those and signed zeros else.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
+ep_status ep_quantize_fp8(int32_t type, const void *x, int64_t num_rows, int32_t num_cols, int64_t row_stride,
+                          uint32_t flags, uint8_t *codes, float *scales, void *stream);
+
+/* ep_rms_norm -- root-mean-square norm of rows, with the residual's addition.
+ *   x         device, [num_rows, num_cols] of `type`, rows x_stride elements apart.
+ *   residual  the same with residual_stride, or NULL.
+ *   weight    device, [num_cols] of weight_type: `type` or fp32.
+ *   total     device, [num_rows, num_cols] contiguous, of `type`: x + residual.  May
+ *             be x or residual themselves.  Not used without a residual.
+ *   y         device, [num_rows, num_cols] contiguous, of `type`, or NULL.
+ *   codes, scales  device, u8 [num_rows, num_cols] and fp32 [num_rows,
+ *             ceil(num_cols / 128)] row-major, or NULL: y as E4M3 codes, as
+ *             ep_dispatch_prequant takes them.
+ * h = x + residual; y = h * weight / sqrt(mean(h^2) + eps), eps > 0.  All of it is
+ * fp32: total and y are rounded once, y is formed from the unrounded h, and the
+ * codes are those of ep_quantize_fp8 for the unrounded y.  Rows whose squares leave
+ * fp32 are scaled by a power of two first.  A row holding NaN gives NaN; one
+ * holding infinities NaN for those and zeros else.
+ * num_cols is at most EP_MAX_NORM_COLS.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
+ep_status ep_rms_norm(int32_t type, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                      const void *weight, int32_t weight_type, float eps, int64_t num_rows, int32_t num_cols,
+                      void *total, void *y, uint8_t *codes, float *scales, void *stream);
+
+/* ep_rms_norm_backward -- gradients of ep_rms_norm.
+ *   x            what was normalised: x, or total where a residual was added.
+ *   grad         device, [num_rows, num_cols] of `type`: the gradient of y.
+ *   grad_total   the same, or NULL: the gradient that reaches total past the norm.
+ *   grad_x       device, [num_rows, num_cols] contiguous, of `type`: the gradient of
+ *                x, and of the residual too.  May be grad or grad_total themselves.
+ *   grad_weight  device, fp32 [num_cols]; zeros for no rows.
+ *   workspace    device, 4-byte aligned, of the size that
+ *                ep_rms_norm_backward_workspace gives for these sizes; free again
+ *                when the call's work is done.
+ * With i = 1 / sqrt(mean(x^2) + eps) and n = x i:
+ *   grad_x = i (grad weight - n mean(grad weight n)) + grad_total,
+ *   grad_weight = sum over rows of grad n, in fp32 in a fixed order.
+ * Errors as ep_rms_norm. */
+ep_status ep_rms_norm_backward_workspace(int32_t type, int64_t num_rows, int32_t num_cols, int64_t *bytes);
+ep_status ep_rms_norm_backward(int32_t type, const void *x, int64_t x_stride, const void *weight, int32_t weight_type,
+                               float eps, const void *grad, int64_t grad_stride, const void *grad_total,
+                               int64_t grad_total_stride, int64_t num_rows, int32_t num_cols, void *grad_x,
+                               float *grad_weight, void *workspace, void *stream);
 
 /* ep_handle_free -- waits for the handle's own layout work, then releases its
  * device and pinned host memory.  The caller guarantees no other call using
