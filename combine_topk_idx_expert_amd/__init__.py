@@ -41,6 +41,8 @@ from ._native import (  # noqa: F401
     get_layout,
     lib,
     lib_path,
+    matmul,
+    matmul_fp8,
     matmul_int8,
     quantize_fp8,
     quantize_int8,

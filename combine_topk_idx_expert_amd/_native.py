@@ -209,7 +209,9 @@ def lib() -> ctypes.CDLL:
         L.ep_rms_norm.argtypes = [i32, vp, i64, vp, i64, vp, i32, f32, i64, i32, vp, vp, vp, vp, vp]
         L.ep_rms_norm_backward_workspace.argtypes = [i32, i64, i32, ctypes.POINTER(i64)]
         L.ep_rms_norm_backward.argtypes = [i32, vp, i64, vp, i32, f32, vp, i64, vp, i64, i64, i32, vp, vp, vp, vp]
-        for fn in ("ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
+        L.ep_matmul_fp8.argtypes = [vp, vp, i64, vp, vp, i32, vp, vp, i32, i32, u32, i32, vp, vp]
+        L.ep_matmul.argtypes = [i32, vp, i64, vp, i32, vp, vp, i32, i32, u32, vp, vp, vp]
+        for fn in ("ep_matmul_fp8", "ep_matmul", "ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
             getattr(L, fn).restype = i32
         L.ep_debug_e4m3_encode.argtypes = [vp, vp, i64, vp]
         L.ep_debug_e4m3_encode.restype = i32
@@ -922,6 +924,119 @@ def rms_norm_backward(x, weight, grad, eps: float = 1e-6, grad_total=None, out=N
     _launch(device, lib().ep_rms_norm_backward, code, x.data_ptr(), stride, weight.data_ptr(), wcode, eps, grad.data_ptr(),
             gstride, _ptr(grad_total), tstride, N, H, gx.data_ptr(), gw.data_ptr(), space.data_ptr())
     return gx, gw
+
+
+def _product(x, w, rows, gated, names=("a", "w")):
+    """Checked sizes of a product's operands: (M, inner, G, outer, width, row_start, row_count)."""
+    import torch
+
+    if not (isinstance(x, torch.Tensor) and isinstance(w, torch.Tensor)):
+        raise TypeError(f"{names[0]} and {names[1]} must be torch.Tensors")
+    xshape, shape = x.shape, w.shape
+    if len(xshape) != 2:
+        raise ValueError(f"{names[0]} must have 2 dimensions, got {tuple(xshape)}")
+    start = count = None
+    G = 0
+    if rows is not None:
+        if len(shape) != 3 or shape[0] == 0:
+            raise ValueError(f"{names[1]} must have shape [groups, outer, inner], got {tuple(shape)}")
+        G = shape[0]
+        start, count = rows
+        _require(start, torch.int64, (G,), "row_start", x.device)
+        _require(count, torch.int32, (G,), "row_count", x.device)
+    elif len(shape) != 2:
+        raise ValueError(f"{names[1]} must have shape [outer, inner], got {tuple(shape)}")
+    if shape[-1] != xshape[1]:
+        raise ValueError(f"{names[1]} has an inner size of {shape[-1]}, {names[0]} of {xshape[1]}")
+    N = shape[-2]
+    if gated and N % 2:
+        raise ValueError(f"a gated product needs an even number of channels, got {N}")
+    return xshape[0], xshape[1], G, N, N // 2 if gated else N, start, count
+
+
+_e4m3_types: tuple = ()
+
+
+def _require_codes(t, shape, name, device=None):
+    """E4M3 codes: uint8, or torch's float8_e4m3fn, which has the same bytes."""
+    import torch
+
+    global _e4m3_types
+    if not _e4m3_types:
+        _e4m3_types = (torch.uint8, torch.float8_e4m3fn)
+    if t.dtype not in _e4m3_types:
+        raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
+    _require(t, t.dtype, shape, name, device)
+
+
+def matmul_fp8(a, w, rows=None, gated: bool = False, scales_col_major: bool = False, out_dtype=None, out=None):
+    """ep_matmul_fp8: a = (codes [M, inner], scales float32 [M, B], or [B, M] with
+    scales_col_major) as dispatch (fp8) and quantize_fp8 make them, times w = (codes [outer,
+    inner], scales float32 [C, B]), or, with rows = (row_start int64 [G], row_count int32 [G]) as
+    expert_rows gives them, w = (codes [G, outer, inner], scales float32 [G, C, B]) -> [M, outer].
+    Codes are uint8 or float8_e4m3fn; B = ceil(inner / 128), C = ceil(outer / 128).
+
+    gated: silu(first half of the channels) * second half -> [M, outer / 2]; each half has blocks
+    of its own, C = 2 * ceil(outer / 2 / 128).  out_dtype: bfloat16 (default), float16 or float32.
+    Rows of no group are left as they were in ``out`` (without ``out`` they are not initialised)."""
+    import torch
+
+    if not (isinstance(a, tuple) and len(a) == 2 and isinstance(w, tuple) and len(w) == 2):
+        raise TypeError("a and w must be pairs (codes, scales)")
+    x, xs = a
+    wc, wsc = w
+    M, K, G, N, width, start, count = _product(x, wc, rows, gated, ("a codes", "w codes"))
+    device, kb = x.device, _blocks(K)
+    _require_codes(x, x.shape, "a codes")
+    _require(xs, torch.float32, (kb, M) if scales_col_major else (M, kb), "a scales", device)
+    _require_codes(wc, wc.shape, "w codes", device)
+    nb = 2 * _blocks(width) if gated else _blocks(N)
+    _require(wsc, torch.float32, (G, nb, kb) if G else (nb, kb), "w scales", device)
+    if out is None:
+        out = torch.empty_strided((M, width), (width, 1), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                                  device=device)
+    else:
+        _require(out, out.dtype if out_dtype is None else out_dtype, (M, width), "out", device)
+    code = _type(out.dtype, "out")
+    _launch(device, lib().ep_matmul_fp8, x.data_ptr(), xs.data_ptr(), M, wc.data_ptr(), wsc.data_ptr(), G,
+            _ptr(start), _ptr(count), K, N, (_GATED if gated else 0) | (_FP8_COL_MAJOR if scales_col_major else 0), code,
+            out.data_ptr())
+    return out
+
+
+def _half(t, name):
+    code = _type(t.dtype, name)
+    if code == 0:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def matmul(a, w, rows=None, gated: bool = False, pre=None, out=None):
+    """ep_matmul: a [M, inner] times w [outer, inner], or, with rows = (row_start int64 [G],
+    row_count int32 [G]) as expert_rows gives them, w [G, outer, inner] -> [M, outer]; bfloat16 or
+    float16, sums in float32.
+
+    gated: silu(first half of the channels) * second half -> [M, outer / 2].  pre: optional [M,
+    outer], takes the product before the gate, which matmul_backward wants.  Rows of no group are
+    left as they were in ``out`` and ``pre`` (without ``out`` they are not initialised)."""
+    import torch
+
+    M, K, G, N, width, start, count = _product(a, w, rows, gated)
+    device, dtype = a.device, a.dtype
+    code = _half(a, "a")
+    _require(a, dtype, a.shape, "a")
+    _require(w, dtype, w.shape, "w", device)
+    if pre is not None:
+        if not gated:
+            raise ValueError("pre belongs to a gated product")
+        _require(pre, dtype, (M, N), "pre", device)
+    if out is None:
+        out = torch.empty_strided((M, width), (width, 1), dtype=dtype, device=device)
+    else:
+        _require(out, dtype, (M, width), "out", device)
+    _launch(device, lib().ep_matmul, code, a.data_ptr(), M, w.data_ptr(), G, _ptr(start), _ptr(count), K, N,
+            _GATED if gated else 0, _ptr(pre), out.data_ptr())
+    return out
 
 
 def debug_e4m3_encode(q):

@@ -10,7 +10,7 @@ import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = [os.path.join(PKG, "csrc", f) for f in ("ep_api.hip", "ep_norm.hip")]
+SRC = [os.path.join(PKG, "csrc", f) for f in ("ep_api.hip", "ep_half.hip", "ep_fp8.hip", "ep_norm.hip")]
 LIB = os.path.join(PKG, "libep_mi355x.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

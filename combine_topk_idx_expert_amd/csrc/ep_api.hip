@@ -19,8 +19,8 @@
 #include "ep_dispatch.hpp"
 #include "ep_host.hpp"
 #include "ep_int8.hpp"
-#include "ep_int8_tile.hpp"
 #include "ep_layout.hpp"
+#include "ep_product_launch.hpp"
 #include "ep_route.hpp"
 
 using namespace ep;
@@ -764,11 +764,11 @@ ep_status ep_matmul_int8(const int8_t* a, const float* a_scale, int64_t num_rows
   if (misaligned(a, 16) || misaligned(w, 16) || misaligned(out, 16) || misaligned(a_scale, 4) ||
       misaligned(w_scale, 4) || misaligned(row_start, 8) || misaligned(row_count, 4))
     return fail(EP_ERR_SHAPE, "a / w / out must be 16-byte aligned, other arrays aligned to their element size");
-  MatmulArgs m{a, a_scale, w, w_scale, num_groups > 0 ? row_start : nullptr, num_groups > 0 ? row_count : nullptr,
-               out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer, 0, num_rows};
+  MatmulArgs m{(const uint8_t*)a, a_scale, (const uint8_t*)w, w_scale, num_groups > 0 ? row_start : nullptr, num_groups > 0 ? row_count : nullptr,
+               out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer, 0, num_rows, nullptr, 0, 0};
   return with_type(out_type, [&](auto io) {
-    return gated ? launch_matmul<decltype(io), true>(m, (hipStream_t)stream)
-                 : launch_matmul<decltype(io), false>(m, (hipStream_t)stream);
+    return gated ? launch_matmul<Int8Math, decltype(io), true>(m, (hipStream_t)stream)
+                 : launch_matmul<Int8Math, decltype(io), false>(m, (hipStream_t)stream);
   });
 }
 

@@ -1,0 +1,233 @@
+// ep_fp8_tile.hpp -- product of E4M3 rows with block scales in tiles staged
+// through LDS.
+#pragma once
+
+#include "ep_product_tile.hpp"
+
+namespace ep {
+
+// A workgroup of WM x WN waves computes tiles of BM rows x BN channels, one after the
+// other, in steps of a block of 128 channels of the inner dimension; the steps of all
+// its tiles form one stream, as in ep_product_tile.hpp.  A step is one matrix
+// instruction for each 16 x 16 of a wave's share, and what it gives is scaled and added
+// to the fp32 sums by vector instructions while the next ones run.
+//
+// Two stages of LDS (a step each).  A wave goes through its row tiles in order; before
+// the last two it has all fragments of the step in registers, waits for its own loads of
+// the next step, and meets the others: then the next step may be read and this one's
+// stage loaded over.  So a load has about a step to arrive, and fragments are read two
+// row tiles ahead, those of the weights behind their last use.
+//
+// LDS image: 128 bytes a row, chunk ^ (row & 7).  Columns of a wave's channel tiles, rows
+// past the group's and channels past the last as in ep_product_tile.hpp.  Behind the rows
+// a stage holds their scales of the block, and the two of the weights: of the tile's two
+// blocks of columns, or of its gates and its ups.
+template <int BM, int BN, int WM, int WN>
+struct Fp8Shape {
+  static constexpr int kWaves = WM * WN;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+  static constexpr int CW = BN / WN;
+  static constexpr int kRowBytes = 128;
+  static constexpr int kScaleAt = (BM + BN) * kRowBytes;
+  static constexpr int kStage = kScaleAt + kThreads * 4;
+  static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;  // direct loads a wave and step
+  static constexpr int kLoads = kLoadsA + kLoadsW + 1;                        // and one of scales
+  static_assert(BM / kWave < kWaves, "a wave is left for the weights' scales");
+  static size_t lds(int groups) { return 2 * (size_t)kStage + ((size_t)groups + 1) * 4; }
+};
+
+template <typename AR, typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
+__global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, int n_tiles) {
+  typedef Fp8Shape<BM, BN, WM, WN> S;
+  constexpr int MT = S::MT, NT = S::NT, CW = S::CW;
+  constexpr int BC = GATED ? BN / 2 : BN;  // columns of out
+  constexpr int NO = GATED ? NT / 2 : NT;  // column tiles of out a wave
+  static_assert(MT % 4 == 0, "fragment registers take turns, also in half tiles");
+  static_assert(BC <= 256 && 128 % (16 * NO) == 0, "a wave's columns lie in one block");
+  extern __shared__ uint8_t tile_lds[];
+  int* const pre = (int*)(tile_lds + 2 * S::kStage);
+  const int lane = lane_id();
+  const int wave = uniform((int)threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int q = lane >> 4, r = lane & 15;
+
+  tile_starts<S::kThreads, BM>(a, pre);
+  const int total = uniform(pre[a.G]) * n_tiles;
+  const int K = a.K;
+  const int steps = (K + 127) / 128;
+  const int per = gridDim.x / 8;
+  const int slot = gridDim.x % 8 == 0 ? ((int)blockIdx.x % 8) * per + (int)blockIdx.x / 8 : (int)blockIdx.x;
+  if (slot >= total) return;
+
+  // ---- producer: the stream of loads
+  const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+  const uint32_t lane_off = (uint32_t)(lane >> 3) * K + chunk;
+  const uint32_t lane_off_w = (uint32_t)((lane >> 5) * 4 * NO + ((lane >> 3) & 3)) * K + chunk;
+  int p_tile = slot, p_step = steps;
+  uint32_t p_stage = 0;
+  __amdgpu_buffer_rsrc_t ra, rw, ru;
+  const float* p_scale = a.a_scale;  // this lane's scale of the stream's next step
+  int64_t p_scale_step = 0;
+  auto next_tile = [&]() {
+    const bool any = p_tile < total;
+    const Tile x = locate<BM, BC>(a, pre, n_tiles, any ? p_tile : slot);
+    const uint8_t* w = a.w + (int64_t)x.g * a.N * K;
+    ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
+    rw = buffer_of(w + (int64_t)x.c0 * K, any ? (int64_t)x.cols * K : 0);
+    if (GATED) ru = buffer_of(w + (int64_t)(x.c0 + a.width) * K, any ? (int64_t)x.cols * K : 0);
+    // (rows and columns past the tile's have the scale of its last)
+    if (wave < BM / kWave) {
+      p_scale = a.a_scale + (x.m0 + min(wave * kWave + lane, x.rows - 1)) * a.a_row_step;
+      p_scale_step = a.a_block_step;
+    } else {
+      const int col = GATED ? x.c0 : min(x.c0 + (lane & 1) * 128, a.width - 1);
+      p_scale = block_scales(a, GATED, x.g, col, GATED && (lane & 1));
+      p_scale_step = 1;
+    }
+    p_tile += gridDim.x;
+    p_step = 0;
+  };
+  // load i of this wave's kLoads for the next step of the stream
+  auto load_one = [&](int i) {
+    const uint32_t k0 = (uint32_t)p_step * 128;
+    uint8_t* st = tile_lds + p_stage;
+    if (i == S::kLoads - 1) {
+      __builtin_amdgcn_global_load_lds((global_byte*)p_scale, (lds_byte*)(st + S::kScaleAt + wave * kWave * 4), 4, 0, 0);
+    } else if (i < S::kLoadsA) {
+      const int row = (i * S::kWaves + wave) * 8;
+      uint32_t off = lane_off + k0;
+      asm("" : "+v"(off));  // one register and an addition a load, rather than a register a load
+      load16_to_lds(ra, st + row * S::kRowBytes, k0 + chunk < (uint32_t)K ? off + (uint32_t)row * K : kBeyond);
+    } else {
+      // LDS rows `row` + 0..7: half of column tile n of wave column v
+      const int row = ((i - S::kLoadsA) * S::kWaves + wave) * 8;
+      const int v = row / CW, n = row % CW / 16, half = row % 16 / 8;
+      uint32_t off = lane_off_w + k0;
+      asm("" : "+v"(off));
+      off += (uint32_t)(v * 16 * NO + n % NO * 4 + half * 8 * NO) * K;
+      load16_to_lds(GATED && n >= NO ? ru : rw, st + (BM + row) * S::kRowBytes, k0 + chunk < (uint32_t)K ? off : kBeyond);
+    }
+  };
+  auto advance = [&]() {
+    ++p_step;
+    p_scale += p_scale_step;
+    p_stage ^= S::kStage;
+  };
+
+  // ---- consumer
+  const uint32_t frag = r * S::kRowBytes + (q ^ (r & 7)) * 16;  // first half of a step; the second: ^ 64
+  const uint32_t a_lane = wm * (MT / 2) * 16 * S::kRowBytes + frag;
+  const uint32_t w_lane = (BM + wn * CW) * S::kRowBytes + frag;
+  const uint32_t sa_lane = S::kScaleAt + (wm * (MT / 2) * 16 + r) * 4;
+  uint32_t cur = 0;  // the current stage
+  f32x4 acc[MT][NT], p[NT];
+  typename AR::frag av[2], wv[NT];
+  float sa[2], sw[2], s_prev[2];
+  auto row_of = [](int m) { return m < MT / 2 ? m * 16 : (m - MT / 2) * 16 + BM / 2; };
+  auto read_a = [&](uint32_t stage, int slot_, int m) {
+    const uint32_t at = stage + a_lane + row_of(m) * S::kRowBytes;
+    av[slot_] = AR::make(*(const i32x4*)(tile_lds + at), *(const i32x4*)(tile_lds + (at ^ 64)));
+    sa[slot_] = *(const float*)(tile_lds + stage + sa_lane + row_of(m) * 4);
+  };
+  auto read_w = [&](uint32_t stage, int n) {
+    const uint32_t at = stage + w_lane + n * 16 * S::kRowBytes;
+    wv[n] = AR::make(*(const i32x4*)(tile_lds + at), *(const i32x4*)(tile_lds + (at ^ 64)));
+  };
+  auto read_sw = [&](uint32_t stage) {
+    const float* s = (const float*)(tile_lds + stage + S::kScaleAt) + BM;
+    sw[0] = s[GATED ? 0 : wn * 16 * NO / 128];
+    sw[1] = s[GATED ? 1 : wn * 16 * NO / 128];
+  };
+  auto add = [&](int m) {  // the products in p, of row tile m, to the sums
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = __builtin_fmaf(p[n][i], s_prev[n / NO], acc[m][n][i]);
+  };
+  // One step of MTN row tiles.
+  auto step = [&](auto mtn) {
+    constexpr int MTN = decltype(mtn)::value;
+    const uint32_t next = cur ^ S::kStage;
+#pragma unroll
+    for (int u = 0; u < MTN; ++u) {
+      if (u == MTN - 2) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (p_step == steps) next_tile();
+      }
+      const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int before = u == 0 ? MTN - 1 : u - 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[before][n][i] = __builtin_fmaf(p[n][i], s_prev[n / NO], acc[before][n][i]);
+        p[n] = AR::mfma128(wv[n], av[u % 2]);
+        if (u == MTN - 1) read_w(next, n);
+      }
+      s_prev[0] = s0;
+      s_prev[1] = s1;
+      if (u == MTN - 1) read_sw(next);
+      if (u + 2 < MTN)
+        read_a(cur, u % 2, u + 2);
+      else
+        read_a(next, u % 2, u + 2 - MTN);
+      if (u >= MTN - 2) {
+#pragma unroll
+        for (int i = u - (MTN - 2); i < S::kLoads; i += 2) load_one(i);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    advance();
+    cur = next;
+  };
+
+  // the first two steps of the stream, and the first fragments
+  for (int s = 0; s < 2; ++s) {
+    if (p_step == steps) next_tile();
+    for (int i = 0; i < S::kLoads; ++i) load_one(i);
+    advance();
+  }
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kLoads) : "memory");
+#pragma unroll
+  for (int n = 0; n < NT; ++n) read_w(0, n);
+  read_sw(0);
+  read_a(0, 0, 0);
+  read_a(0, 1, 1);
+
+  for (int t = slot; t < total; t += gridDim.x) {
+    const Tile x = locate<BM, BC>(a, pre, n_tiles, t);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) p[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    s_prev[0] = s_prev[1] = 0.0f;
+    if (!HALVES || x.rows > BM / 2) {
+      for (int s = 0; s < steps; ++s) step(std::integral_constant<int, MT>{});
+      add(MT - 1);
+    } else {
+      constexpr int kHalf = HALVES ? MT / 2 : MT;
+      for (int s = 0; s < steps; ++s) step(std::integral_constant<int, kHalf>{});
+      add(kHalf - 1);
+    }
+
+    int er = r, eq = q;
+    asm volatile("" : "+v"(er), "+v"(eq));  // what follows is not kept in registers over the steps
+    const int col = wn * 16 * NO + eq * 4 * NO;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = wm * (MT / 2) * 16 + row_of(m) + er;
+      if (row >= x.rows) continue;
+      float y[NT * 4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[n * 4 + i] = acc[m][n][i];
+      store_row<IO, GATED, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+}
+
+}  // namespace ep

@@ -1,20 +1,9 @@
-// ep_ops_launch.hpp -- argument checks and launch configuration of the routing
-// and int8 operators.
+// ep_ops_launch.hpp -- argument checks and launch configuration of the router and
+// of int8 quantising.
 //
 // Part of ep_api.hip's translation unit: it is included there, inside the
 // anonymous namespace, after the error helpers (fail, EP_LAUNCHED) it uses.
 #pragma once
-
-ep_status validate_matmul(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags) {
-  if (flags & ~(uint32_t)EP_MATMUL_GATED) return fail(EP_ERR_SHAPE, "unknown matmul flags 0x%x", flags);
-  if (num_rows < 0 || num_groups < 0 || num_groups > EP_MAX_EXPERTS)
-    return fail(EP_ERR_SHAPE, "bad sizes: %lld rows, %d groups (at most %d)", (long long)num_rows, num_groups,
-                EP_MAX_EXPERTS);
-  if (outer < 1 || outer > EP_MAX_MATMUL_OUTER || ((flags & EP_MATMUL_GATED) && outer % 2 != 0))
-    return fail(EP_ERR_SHAPE, "outer %d must lie in [1, %d] and be even for a gated product", outer, EP_MAX_MATMUL_OUTER);
-  if (num_rows >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "num_rows %lld reaches 2^31", (long long)num_rows);
-  return EP_OK;
-}
 
 ep_status validate_route(const ep_route_config* c, int32_t type, int64_t num_tokens, int64_t row_stride) {
   if (!c) return fail(EP_ERR_NULL, "route config is NULL");
@@ -152,127 +141,4 @@ ep_status launch_quantize(const QuantArgs& a, hipStream_t s) {
   quantize_kernel<IO><<<(int)a.N, kQuantThreads, 0, s>>>(a);
   EP_LAUNCHED("quantize_kernel");
   return EP_OK;
-}
-
-template <typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
-ep_status launch_matmul_tile(const MatmulArgs& a, hipStream_t s) {
-  typedef TileShape<BM, BN, WM, WN> S;
-  const int bc = GATED ? BN / 2 : BN;
-  const int64_t n_tiles = (a.width + bc - 1) / bc;
-  const int64_t most = (a.M / BM + a.G) * n_tiles;  // each group's last row tile may be partly filled
-  if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "product of %lld tiles is too large", (long long)most);
-  const int grid = (int)std::min<int64_t>(most, kCUs);
-  matmul_tile_kernel<IO, GATED, BM, BN, WM, WN, HALVES><<<grid, S::kThreads, S::lds(a.G), s>>>(a, (int)n_tiles);
-  EP_LAUNCHED("matmul_tile_kernel");
-  return EP_OK;
-}
-
-template <typename IO, bool GATED, int MT, int NT, int KW, int S>
-ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
-  const int bc = (GATED ? NT / 2 : NT) * 16;
-  const int64_t nb = (a.width + bc - 1) / bc;
-  // row tiles side by side; a workgroup takes several where there are more.  For
-  // groups: twice the mean, or what fills the card
-  int64_t y = std::min<int64_t>((std::min(a.M, a.most) + 16 * MT - 1) / (16 * MT), 4096);
-  if (a.row_start)
-    y = std::min(y, std::max<int64_t>((2 * a.M / a.G + 16 * MT - 1) / (16 * MT), 32 * kCUs / (nb * a.G) + 1));
-  matmul_split_kernel<IO, GATED, MT, NT, KW, S><<<dim3((unsigned)nb, (unsigned)y, a.G), KW * kWave, 0, s>>>(a);
-  EP_LAUNCHED("matmul_split_kernel");
-  return EP_OK;
-}
-
-// Which kernel (both sides measured on MI355X):
-//  - tiles of 256 x 256 once they fill three quarters of the CUs; below that
-//    tiles of 128 x 256 while they fill three eighths (2048 x 7168 x 4096 gated: 67
-//    against 82 us; 8192 x 8192 x 8192: 256 x 256 by 10%);
-//  - below that, and for at most 64 rows whatever the width, the split over the inner
-//    size (512 x 7168 x 4096 gated: 23 us against 54 and 79; 64 rows: 9 against 44 and
-//    49; 1 x 7168 x 49152: 63 against 88 and 90, 64 rows of it 87 against 91 and 93).
-// Groups: their sizes are on the device.  A group of at most kFewRows rows is
-// the split's and a larger one the tiles'; each launch passes over the others'
-// groups.  No second launch where large groups cannot fill more than half of the tiles'
-// grid (8 groups of 72 rows, 7168 x 4096 gated: 72 us by the split alone, 84 by both),
-// or three eighths for tall groups, whose rows the split takes 64 at a time (8 of 1696,
-// 4672 x 318 gated: 46 us by tiles, 80 by the split); nor a first one where the mean
-// is so large that few groups are small.  129 random shapes (2 to 64 groups, inner 320
-// to 7168): with 96 to 128 tiles of large groups, tiles take 1.28 times the split's time
-// for means of up to 128 rows, 1.03 for 129 to 199, 0.72 above; with fewer 1.22, 1.22 and
-// 0.97, with up to 192 1.00, 0.85 and 0.72.  The rule is within 10% of the fastest of the
-// three in 106 of them and 4% off on average (at worst 1.6 times: 32 groups of 112
-// rows, 2048 x 256, by the split 35 us, by tiles 22).
-constexpr int64_t kFewRows = 64;
-
-// The split's tile, MT x NT sixteens of rows and channels.  Its time is that of the
-// loads, MT + NT for each step of a workgroup, on the CU with the most workgroups:
-// the shape for which that is least.  1 x 7168 x 4096 gated: 1 x 2 7.4 us, 1 x 4 9.0;
-// 64 rows: 2 x 2 9.0, 1 x 2 10.5, 2 x 4 9.8, 4 x 4 12.6; 512 rows: 4 x 4 23, 2 x 4 35;
-// 3475 x 6432 x 99: 2 x 4 14, 4 x 4 18.
-// Two waves a workgroup leave room for several workgroups a CU.  Four are better
-// where weights that no cache holds stream through a long inner size (one row: 7.4
-// against 9.4 us; 32 groups of 3 rows: 154 against 160; from the L2, 8 groups of 79
-// rows, 3904 x 78: 9.3 against 7.1) and a CU has one workgroup or small ones (512
-// rows, two a CU: 27 against 23).
-template <typename IO, bool GATED, int MT, int NT>
-ep_status launch_matmul_split(const MatmulArgs& a, int64_t blocks, hipStream_t s) {
-  const bool stream = a.K >= 2048 && (int64_t)a.G * a.N * a.K >= (int64_t)8 << 20;
-  return stream && (MT == 1 || blocks <= kCUs) ? launch_matmul_split<IO, GATED, MT, NT, 4, 2>(a, s)
-                                               : launch_matmul_split<IO, GATED, MT, NT, 2, 2>(a, s);
-}
-
-template <typename IO, bool GATED>
-ep_status launch_matmul_few(const MatmulArgs& a, hipStream_t s) {
-  constexpr int kShapes[5][2] = {{1, 2}, {1, 4}, {2, 2}, {2, 4}, {4, 4}};
-  const int64_t mean = std::min(a.M / a.G + (a.M % a.G != 0), a.most);
-  int64_t least = INT64_MAX, blocks = 0;
-  int best = 0;
-  for (int i = 0; i < 5; ++i) {
-    const int rows = 16 * kShapes[i][0], cols = (GATED ? 8 : 16) * kShapes[i][1];
-    const int64_t n = (mean + rows - 1) / rows * a.G * ((a.width + cols - 1) / cols);
-    const int64_t cost = (n + kCUs - 1) / kCUs * (kShapes[i][0] + kShapes[i][1]);
-    if (cost > least) continue;  // (of equals the larger one)
-    least = cost;
-    blocks = n;
-    best = i;
-  }
-  switch (best) {
-    case 0: return launch_matmul_split<IO, GATED, 1, 2>(a, blocks, s);
-    case 1: return launch_matmul_split<IO, GATED, 1, 4>(a, blocks, s);
-    case 2: return launch_matmul_split<IO, GATED, 2, 2>(a, blocks, s);
-    case 3: return launch_matmul_split<IO, GATED, 2, 4>(a, blocks, s);
-    default: return launch_matmul_split<IO, GATED, 4, 4>(a, blocks, s);
-  }
-}
-
-// EP_KERNEL_* of the launches for M rows in G groups (0: dense) and `width` columns of out.
-uint32_t matmul_kernels(int64_t M, int G, int width, bool gated) {
-  const int bc = gated ? 128 : 256;
-  const int64_t n_tiles = (width + bc - 1) / bc;
-  if (G == 0) {
-    if (M <= kFewRows) return EP_KERNEL_SPLIT;
-    if ((M + 255) / 256 * n_tiles >= 3 * kCUs / 4) return EP_KERNEL_TILES_256;
-    if ((M + 127) / 128 * n_tiles >= 3 * kCUs / 8) return EP_KERNEL_TILES_128;
-    return EP_KERNEL_SPLIT;
-  }
-  const int64_t mean = M / G;
-  // row tiles that large groups can fill: a tile has more than kFewRows rows
-  const int64_t large = std::min(M / 256 + G, M / (kFewRows + 1));
-  if (mean <= 2 * kFewRows ? large * n_tiles <= kCUs / 2 : large * n_tiles < 3 * kCUs / 8) return EP_KERNEL_SPLIT;
-  return ((M / 256 + G) * n_tiles >= 3 * kCUs / 4 ? EP_KERNEL_TILES_256 : EP_KERNEL_TILES_128) |
-         (mean < 4 * kFewRows ? EP_KERNEL_SPLIT : 0);
-}
-
-template <typename IO, bool GATED>
-ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
-  const uint32_t kernels = matmul_kernels(a.M, a.row_start ? a.G : 0, a.width, GATED);
-  a.least = 0;
-  a.most = a.M;
-  if (kernels & EP_KERNEL_SPLIT) {
-    MatmulArgs few = a;
-    if (kernels != EP_KERNEL_SPLIT) few.most = kFewRows;
-    const ep_status st = launch_matmul_few<IO, GATED>(few, s);
-    if (st != EP_OK || kernels == EP_KERNEL_SPLIT) return st;
-    a.least = kFewRows + 1;
-  }
-  if (kernels & EP_KERNEL_TILES_256) return launch_matmul_tile<IO, GATED, 256, 256, 2, 4, true>(a, s);
-  return launch_matmul_tile<IO, GATED, 128, 256, 2, 4, false>(a, s);
 }

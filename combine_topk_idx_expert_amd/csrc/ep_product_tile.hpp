@@ -1,9 +1,9 @@
-// ep_int8_tile.hpp -- int8 product in tiles staged through LDS.
+// ep_product_tile.hpp -- products of int8 and of 16-bit rows in tiles staged through LDS.
 #pragma once
 
 #include <type_traits>
 
-#include "ep_int8.hpp"
+#include "ep_product.hpp"
 
 namespace ep {
 
@@ -20,7 +20,7 @@ namespace ep {
 // So a load has two steps to arrive, no fragment is waited for behind a
 // barrier, and the next tile's first steps arrive during a tile's epilogue.
 //
-// What bounds it: a step takes 1470 cycles (256 x 256; 990 at 128 x 256) against 1024
+// What bounds it for int8: a step takes 1470 cycles (256 x 256; 990 at 128 x 256) against 1024
 // (512) of products.  The direct loads alone come at ~24 bytes a clock and CU (a
 // probe of them from the L2: 42 to 54), and more stages change nothing; and
 // under int8 products the clock falls to 1.7-1.9 GHz of 2.4.  65536 rows of 64 groups,
@@ -35,7 +35,7 @@ namespace ep {
 //
 // Rows beyond the group's last one and channels beyond the last are beyond the
 // buffer descriptor's size and arrive as zeros; so do chunks of A past the
-// inner size (those of W may hold anything, their partners are zero).
+// inner size (those of W may hold anything for int8, where their partners are zero).
 //
 // Row tiles of a wave: mt = 0..MT-1, in two halves of the tile, so that a tile
 // with at most BM / 2 rows costs half the products (HALVES).
@@ -60,7 +60,9 @@ struct TileShape {
   static constexpr int kLoads = kLoadsA + kLoadsW;
   static constexpr int kScales = BM + BN;  // floats of a tile
   static_assert(kLoadsA >= 1 && kLoadsW >= 1, "a load covers 16 rows");
-  static size_t lds(int groups) { return kStages * ((size_t)kStage + kScales * 4) + ((size_t)groups + 1) * 4; }
+  static size_t lds(int groups, bool scaled) {
+    return kStages * ((size_t)kStage + (scaled ? kScales * 4 : 0)) + ((size_t)groups + 1) * 4;
+  }
 };
 
 __device__ __forceinline__ int chunk_order(int g) { return ((g ^ (g >> 1)) & 1) * 2 + (g >> 1); }  // 0, 2, 3, 1
@@ -145,7 +147,7 @@ __device__ __forceinline__ Tile locate(const MatmulArgs& a, const int* pre, int 
   return x;
 }
 
-template <typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
+template <typename AR, typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
 __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a, int n_tiles) {
   typedef TileShape<BM, BN, WM, WN> S;
   constexpr int MT = S::MT, NT = S::NT, CW = S::CW;
@@ -154,8 +156,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
   constexpr int kPair = 2 * S::kStage;     // the stages of an even and the next odd step
   static_assert(MT % 4 == 0 && NT == 4, "fragment rings");
   extern __shared__ uint8_t tile_lds[];
+  constexpr bool kScaled = AR::kScales == kRowScales;
+  typedef typename AR::acc acc_t;
   float* const scales = (float*)(tile_lds + S::kStages * S::kStage);  // [kStages][BM + BN]
-  int* const pre = (int*)(scales + S::kStages * S::kScales);
+  int* const pre = (int*)(scales + (kScaled ? S::kStages * S::kScales : 0));
   const int lane = lane_id();
   const int wave = uniform((int)threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
@@ -179,14 +183,14 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
   auto next_tile = [&]() {  // descriptors of tile p_tile, and its scales on their way
     const bool any = p_tile < total;
     const Tile x = locate<BM, BC>(a, pre, n_tiles, any ? p_tile : slot);
-    const int8_t* w = a.w + (int64_t)x.g * a.N * K;
+    const uint8_t* w = a.w + (int64_t)x.g * a.N * K;
     ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
     rw = buffer_of(w + (int64_t)x.c0 * K, any ? (int64_t)x.cols * K : 0);
     if (GATED) ru = buffer_of(w + (int64_t)(x.c0 + a.width) * K, any ? (int64_t)x.cols * K : 0);
     const __amdgpu_buffer_rsrc_t rs = buffer_of(a.a_scale + x.m0, any ? x.rows * 4 : 0);
     const __amdgpu_buffer_rsrc_t rc = buffer_of(a.w_scale + (int64_t)x.g * a.N, any ? a.N * 4 : 0);
     float* dst = scales + p_ring * S::kScales;
-    for (int i = wave; i < S::kScales / kWave; i += S::kWaves) {
+    for (int i = wave; kScaled && i < S::kScales / kWave; i += S::kWaves) {
       int e = i * kWave + lane;
       asm volatile("" : "+v"(e));
       if (i * kWave < BM) {
@@ -217,8 +221,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
       const int v = row / CW, n = row % CW / 16;
       uint32_t offw = lane_off_w + k0;
       asm("" : "+v"(offw));
-      load16_to_lds(GATED && n >= NO ? ru : rw, st + (BM + row) * S::kStep,
-                    offw + (uint32_t)(v * 16 * NO + n % NO * 4) * K);
+      offw += (uint32_t)(v * 16 * NO + n % NO * 4) * K;
+      // (what follows a channel may be NaN; times zero only whole numbers vanish)
+      if (!kScaled && k0 + chunk >= (uint32_t)K) offw = kBeyond;
+      load16_to_lds(GATED && n >= NO ? ru : rw, st + (BM + row) * S::kStep, offw);
     }
   };
   auto advance = [&]() {
@@ -231,7 +237,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
   const uint32_t a_lane = wm * (MT / 2) * 16 * S::kStep + frag;
   const uint32_t w_lane = BM * S::kStep + wn * CW * S::kStep + frag;
   uint32_t pair = 0;  // 0 or kPair: the current pair of stages
-  i32x4 acc[MT][NT], av[4], wv[2][NT];
+  acc_t acc[MT][NT];
+  i32x4 av[4], wv[2][NT];
   auto read_a = [&](uint32_t at, int h, int m) {
     return *(const i32x4*)(tile_lds + at + h * S::kStage + (m < MT / 2 ? m : m - MT / 2 + BM / 32) * 16 * S::kStep);
   };
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
       for (int i = u; i < S::kLoads; i += MTN) load_one(i);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        acc[u][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[h][n], av[u % 4], acc[u][n], 0, 0, 0);
+        acc[u][n] = AR::mfma(wv[h][n], av[u % 4], acc[u][n]);
       __builtin_amdgcn_sched_barrier(0);
     }
     advance();
@@ -278,7 +285,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = i32x4{0, 0, 0, 0};
+      for (int n = 0; n < NT; ++n) acc[m][n] = acc_t{0, 0, 0, 0};
     auto run = [&](auto mtn) {
       for (int s = 0; s < steps; s += 2) {
         step(std::integral_constant<int, 0>{}, mtn);
@@ -302,22 +309,21 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sw[n][i] = sa[BM + (n < NO ? 0 : BC) + col + (n % NO) * 4 + i];
+      for (int i = 0; i < 4; ++i) sw[n][i] = !kScaled ? 1.0f : sa[BM + (n < NO ? 0 : BC) + col + (n % NO) * 4 + i];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = (m < MT / 2 ? 0 : BM / 2) + wm * (MT / 2) * 16 + (m % (MT / 2)) * 16 + er;
       if (row >= x.rows) continue;
-      const float s = sa[row];
-      float v[NO * 4];
+      const float s = kScaled ? sa[row] : 1.0f;
+      float y[NT * 4];
 #pragma unroll
-      for (int n = 0; n < NO; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float y = (float)acc[m][n][i] * s * sw[n][i];
-          if (GATED) y = silu<IO>(y) * ((float)acc[m][n + NT / 2][i] * s * sw[n + NT / 2][i]);
-          v[n * 4 + i] = y;
+          y[n * 4 + i] = (float)acc[m][n][i];
+          if (kScaled) y[n * 4 + i] = y[n * 4 + i] * s * sw[n][i];
         }
-      store_row<IO, NO * 4>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, v);
+      store_row<IO, GATED, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup

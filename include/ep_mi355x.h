@@ -505,6 +505,37 @@ ep_status ep_rms_norm_backward(int32_t type, const void *x, int64_t x_stride, co
                                int64_t grad_total_stride, int64_t num_rows, int32_t num_cols, void *grad_x,
                                float *grad_weight, void *workspace, void *stream);
 
+/* ep_matmul_fp8 -- E4M3 rows times E4M3 weights: what ep_dispatch (fp8) and
+ * ep_quantize_fp8 make, times one matrix for all rows (num_groups 0) or one for the
+ * rows of each group (expert).
+ *   a          device, u8 [num_rows, inner];  a_scale  fp32, for each 128 of inner:
+ *              [num_rows, B] or with EP_FP8_SCALES_COL_MAJOR [B, num_rows], B =
+ *              ceil(inner / 128).
+ *   w          device, u8 [num_groups, outer, inner] ([outer, inner] if num_groups
+ *              is 0);  w_scale  fp32 [num_groups, C, B], one for 128 x 128, C =
+ *              ceil(outer / 128).  With EP_MATMUL_GATED the blocks start anew at the
+ *              second half of the channels: C = 2 ceil(outer / 2 / 128).
+ *   row_start, row_count, out and EP_MATMUL_GATED as in ep_matmul_int8.
+ * y[r][n] = sum over blocks b of a_scale[r][b] w_scale[g][n / 128][b] (sum over the
+ * block's k of a[r][k] w[g][n][k]), in fp32, rounded once to out_type.  A code of NaN
+ * makes NaN of its row's or channel's results.  inner is a multiple of 16; a, w and out
+ * are 16-byte aligned.  Errors as ep_matmul_int8. */
+ep_status ep_matmul_fp8(const uint8_t *a, const float *a_scale, int64_t num_rows, const uint8_t *w,
+                        const float *w_scale, int32_t num_groups, const int64_t *row_start, const int32_t *row_count,
+                        int32_t inner, int32_t outer, uint32_t flags, int32_t out_type, void *out, void *stream);
+
+/* ep_matmul -- rows of `type` (bf16 or fp16) times weights of the same type, as
+ * ep_matmul_fp8 without scales: y[r][n] = sum over k of a[r][k] w[g][n][k] in fp32,
+ * rounded once to `type`.
+ *   pre  device, [num_rows, outer] of `type`, or NULL; with EP_MATMUL_GATED only: y
+ *        before the gate, rounded, which ep_matmul_backward wants.  Rows of no group
+ *        are left as they were.
+ * inner is a multiple of 8; a, w, out and pre are 16-byte aligned.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW, EP_ERR_HIP. */
+ep_status ep_matmul(int32_t type, const void *a, int64_t num_rows, const void *w, int32_t num_groups,
+                    const int64_t *row_start, const int32_t *row_count, int32_t inner, int32_t outer, uint32_t flags,
+                    void *pre, void *out, void *stream);
+
 /* ep_handle_free -- waits for the handle's own layout work, then releases its
  * device and pinned host memory.  The caller guarantees no other call using
  * `h` is still in flight (tutorial 2.6).  NULL is a no-op. */
