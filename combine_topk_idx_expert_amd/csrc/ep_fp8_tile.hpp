@@ -116,9 +116,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   };
 
   // ---- consumer
-  const uint32_t frag = r * S::kRowBytes + (q ^ (r & 7)) * 16;  // first half of a step; the second: ^ 64
-  const uint32_t a_lane = wm * (MT / 2) * 16 * S::kRowBytes + frag;
-  const uint32_t w_lane = (BM + wn * CW) * S::kRowBytes + frag;
+  // the two halves of a step in an image row
+  const uint32_t frag0 = r * S::kRowBytes + (q ^ (r & 7)) * 16, frag1 = frag0 ^ 64;
+  const uint32_t a_at = wm * (MT / 2) * 16 * S::kRowBytes, w_at = (BM + wn * CW) * S::kRowBytes;
   const uint32_t sa_lane = S::kScaleAt + (wm * (MT / 2) * 16 + r) * 4;
   uint32_t cur = 0;  // the current stage
   f32x4 acc[MT][NT], p[NT];
@@ -126,13 +126,13 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   float sa[2], sw[2], s_prev[2];
   auto row_of = [](int m) { return m < MT / 2 ? m * 16 : (m - MT / 2) * 16 + BM / 2; };
   auto read_a = [&](uint32_t stage, int slot_, int m) {
-    const uint32_t at = stage + a_lane + row_of(m) * S::kRowBytes;
-    av[slot_] = AR::make(*(const i32x4*)(tile_lds + at), *(const i32x4*)(tile_lds + (at ^ 64)));
+    const uint8_t* at = tile_lds + (stage + a_at) + row_of(m) * S::kRowBytes;
+    av[slot_] = AR::make(*(const i32x4*)(at + frag0), *(const i32x4*)(at + frag1));
     sa[slot_] = *(const float*)(tile_lds + stage + sa_lane + row_of(m) * 4);
   };
   auto read_w = [&](uint32_t stage, int n) {
-    const uint32_t at = stage + w_lane + n * 16 * S::kRowBytes;
-    wv[n] = AR::make(*(const i32x4*)(tile_lds + at), *(const i32x4*)(tile_lds + (at ^ 64)));
+    const uint8_t* at = tile_lds + (stage + w_at) + n * 16 * S::kRowBytes;
+    wv[n] = AR::make(*(const i32x4*)(at + frag0), *(const i32x4*)(at + frag1));
   };
   auto read_sw = [&](uint32_t stage) {
     const float* s = (const float*)(tile_lds + stage + S::kScaleAt) + BM;
@@ -149,11 +149,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   auto step = [&](auto mtn) {
     constexpr int MTN = decltype(mtn)::value;
     const uint32_t next = cur ^ S::kStage;
+    if (p_step == steps) next_tile();  // (here, since a branch further down lets the sums' additions sink past it)
 #pragma unroll
     for (int u = 0; u < MTN; ++u) {
       if (u == MTN - 2) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (p_step == steps) next_tile();
       }
       const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
 #pragma unroll
