@@ -42,6 +42,7 @@ from ._native import (  # noqa: F401
     lib,
     lib_path,
     matmul,
+    matmul_backward,
     matmul_fp8,
     matmul_int8,
     quantize_fp8,

@@ -211,7 +211,9 @@ def lib() -> ctypes.CDLL:
         L.ep_rms_norm_backward.argtypes = [i32, vp, i64, vp, i32, f32, vp, i64, vp, i64, i64, i32, vp, vp, vp, vp]
         L.ep_matmul_fp8.argtypes = [vp, vp, i64, vp, vp, i32, vp, vp, i32, i32, u32, i32, vp, vp]
         L.ep_matmul.argtypes = [i32, vp, i64, vp, i32, vp, vp, i32, i32, u32, vp, vp, vp]
-        for fn in ("ep_matmul_fp8", "ep_matmul", "ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
+        L.ep_matmul_backward_workspace.argtypes = [i64, i32, u32, ctypes.POINTER(i64)]
+        L.ep_matmul_backward.argtypes = [i32, vp, i64, vp, vp, vp, i32, vp, vp, i32, i32, u32, vp, vp, i32, vp, vp]
+        for fn in ("ep_matmul_fp8", "ep_matmul", "ep_matmul_backward_workspace", "ep_matmul_backward", "ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
             getattr(L, fn).restype = i32
         L.ep_debug_e4m3_encode.argtypes = [vp, vp, i64, vp]
         L.ep_debug_e4m3_encode.restype = i32
@@ -1037,6 +1039,50 @@ def matmul(a, w, rows=None, gated: bool = False, pre=None, out=None):
     _launch(device, lib().ep_matmul, code, a.data_ptr(), M, w.data_ptr(), G, _ptr(start), _ptr(count), K, N,
             _GATED if gated else 0, _ptr(pre), out.data_ptr())
     return out
+
+
+def matmul_backward(a, w, grad, rows=None, gated: bool = False, pre=None, out=None):
+    """ep_matmul_backward: gradients of matmul -> (grad_a [M, inner], grad_w like w).
+
+    grad: that of matmul's result; pre: gated, what matmul kept.  The product's gradient, an
+    operand of both results, is rounded to a's type behind the gate; sums are float32.  out:
+    optional (grad_a, grad_w), either of them None where it is not wanted; grad_w may be float32.
+    Rows of no group are left as they were in grad_a (without ``out`` they are not initialised);
+    grad_w is zero for a group without rows."""
+    import torch
+
+    M, K, G, N, width, start, count = _product(a, w, rows, gated)
+    device, dtype = a.device, a.dtype
+    code = _half(a, "a")
+    _require(a, dtype, a.shape, "a")
+    _require(w, dtype, w.shape, "w", device)
+    _require(grad, dtype, (M, width), "grad", device)
+    if gated:
+        if pre is None:
+            raise ValueError("the gradient of a gated product needs pre")
+        _require(pre, dtype, (M, N), "pre", device)
+    elif pre is not None:
+        raise ValueError("pre belongs to a gated product")
+    gcode = code
+    if out is None:
+        ga = torch.empty_strided((M, K), (K, 1), dtype=dtype, device=device)
+        gw = torch.empty_strided(w.shape, w.stride(), dtype=dtype, device=device)
+    else:
+        ga, gw = out
+        if ga is not None:
+            _require(ga, dtype, (M, K), "grad_a", device)
+        if gw is not None:
+            if gw.dtype == torch.float32:
+                gcode = 0
+            _require(gw, torch.float32 if gcode == 0 else dtype, w.shape, "grad_w", device)
+    space = None
+    if gated:
+        size = ctypes.c_int64()
+        _check(lib().ep_matmul_backward_workspace(M, N, _GATED, ctypes.byref(size)))
+        space = torch.empty(size.value, dtype=torch.uint8, device=device)
+    _launch(device, lib().ep_matmul_backward, code, a.data_ptr(), M, w.data_ptr(), grad.data_ptr(), _ptr(pre), G,
+            _ptr(start), _ptr(count), K, N, _GATED if gated else 0, _ptr(ga), _ptr(gw), gcode, _ptr(space))
+    return ga, gw
 
 
 def debug_e4m3_encode(q):

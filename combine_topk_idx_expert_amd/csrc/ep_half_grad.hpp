@@ -1,0 +1,328 @@
+// ep_half_grad.hpp -- gradients of the 16-bit product: of the rows and of the
+// weights, in tiles staged through LDS; the gate's gradient.
+#pragma once
+
+#include "ep_product_tile.hpp"
+
+namespace ep {
+
+// y = a w^T has the gradients d w (of the rows; inner dimension: channels) and, for
+// each group, d^T a (of its weights; inner dimension: the group's rows).  The inner
+// dimension is not contiguous in w, and in neither operand of d^T a: their stages in
+// LDS are images of 32 inner indexes by BM or BN values, read with ds_read_b64_tr_b16.
+// For 16 lanes that instruction takes four rows of 16 values (lane i: 8 bytes of row
+// i / 4, values 4 (i % 4)..) and gives lane i the four of column i, so two of them make
+// a lane's operand of the matrix instruction.
+//
+// Stream of steps, ring of four stages, order of tiles and halves as in
+// ep_product_tile.hpp, with one difference: a wave's column tiles are 16 neighbouring
+// columns each, and v_permlane16_swap gives a lane eight neighbours of a row at the end.
+//
+// Image of a strided operand: index k has 512 (256) bytes, blocks of 32 bytes (16 values)
+// in the order block ^ f(k), f(k) = k % 4 + 4 (k / 8 % 2): the eight k whose blocks 32
+// lanes read together meet all banks.  Indexes past the end lie past the descriptor, which
+// starts anew at each step, so offsets stay in 32 bits for any number of rows; columns
+// past the last hold the next row's values and are not stored.
+struct Strided {
+  const uint8_t* at;  // the stream's next step
+  int64_t left;       // indexes from there on
+  int64_t stride;     // bytes between indexes
+  int64_t tail;       // bytes of an index from the tile's first value on
+  __device__ __forceinline__ void start(const uint8_t* p, int64_t n, int64_t stride_, int64_t tail_) {
+    at = p;
+    left = n;
+    stride = stride_;
+    tail = tail_;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t step() {
+    const int64_t n = left < 32 ? left : 32;
+    const __amdgpu_buffer_rsrc_t r = buffer_of(at, n > 0 ? (n - 1) * stride + tail : 0);
+    at += 32 * stride;
+    left -= 32;
+    return r;
+  }
+};
+
+// Where lane's 16 bytes of a load of 1 KiB come from, from the step's first index on:
+// loads go round the waves, WIDTH values an index.
+template <int WIDTH>
+__device__ __forceinline__ uint32_t strided_source(int wave, int lane, uint32_t stride) {
+  constexpr int kLanes = WIDTH / 8;  // of an index
+  const int k = wave * (64 / kLanes) + lane / kLanes;
+  const int f = (k & 3) | (k >> 3 & 1) << 2;
+  const int piece = lane % kLanes;
+  return (uint32_t)k * stride + (uint32_t)(((piece >> 1) ^ f) * 2 + (piece & 1)) * 16;
+}
+
+// The byte of the image that lane reads for block `block`: index q * 8 + i / 4, the
+// second half of its operand four indexes on.
+template <int WIDTH>
+__device__ __forceinline__ uint32_t strided_frag(int lane, int block) {
+  const int q = lane >> 4, i = lane & 15;
+  const int f = i >> 2 | (q & 1) << 2;
+  return (uint32_t)(q * 8 + (i >> 2)) * (WIDTH * 2) + (uint32_t)(block ^ f) * 32 + (i & 3) * 8;
+}
+
+template <int WIDTH>
+__device__ __forceinline__ i32x4 read_strided(const uint8_t* at) {
+  typedef short i16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at));
+  const i32x2 hi = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 4 * WIDTH * 2)));
+  return i32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// MatmulArgs here: a = d [M][N], K its row's bytes; w = the weights [G][N][width], or for
+// the weights' gradient the rows a [M][width]; out = [M][width] or [G][N][width].
+//
+// Tile t of the weights' gradient: strips of eight column tiles, in each all row tiles.
+template <int BM, int BN>
+__device__ __forceinline__ Tile locate_weights(const MatmulArgs& a, int m_tiles, int n_tiles, int t) {
+  Tile x;
+  const int each = m_tiles * n_tiles;
+  x.g = t / each;
+  const int in = t - x.g * each;
+  const int strip = in / (8 * m_tiles);
+  const int wide = min(8, n_tiles - strip * 8);
+  const int rest = in - strip * 8 * m_tiles;
+  x.m0 = (int64_t)(rest / wide) * BM;
+  x.rows = min(BM, a.N - (int)x.m0);
+  x.c0 = (strip * 8 + rest % wide) * BN;
+  x.cols = min(BN, a.width - x.c0);
+  return x;
+}
+
+template <typename AR, typename IO, bool WEIGHTS, int BM, int BN, int WM, int WN, bool HALVES>
+__global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, int n_tiles) {
+  typedef TileShape<BM, BN, WM, WN> S;
+  constexpr int MT = S::MT, NT = S::NT;
+  constexpr int kPair = 2 * S::kStage;  // the stages of an even and the next odd step
+  constexpr int kImageA = BM * S::kStep;
+  static_assert(MT % 4 == 0 && NT == 4 && BN == 256 && (BM == 256 || BM == 128), "fragment rings and images");
+  typedef typename AR::acc acc_t;
+  extern __shared__ uint8_t tile_lds[];
+  int* const pre = (int*)(tile_lds + S::kStages * S::kStage);
+  const int lane = lane_id();
+  const int wave = uniform((int)threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int q = lane >> 4, r = lane & 15;
+
+  const int m_tiles = (a.N + BM - 1) / BM;
+  int total;
+  if constexpr (WEIGHTS) {
+    total = a.G * m_tiles * n_tiles;
+  } else {
+    tile_starts<S::kThreads, BM>(a, pre);
+    total = uniform(pre[a.G]) * n_tiles;
+  }
+  const int K = a.K;
+  const int per = gridDim.x / 8;
+  const int slot = gridDim.x % 8 == 0 ? ((int)blockIdx.x % 8) * per + (int)blockIdx.x / 8 : (int)blockIdx.x;
+  if (slot >= total) return;
+
+  auto tile = [&](int t) {
+    if constexpr (WEIGHTS)
+      return locate_weights<BM, BN>(a, m_tiles, n_tiles, t);
+    else
+      return locate<BM, BN>(a, pre, n_tiles, t);
+  };
+  // steps of a tile, even: stages and registers take turns.  (A group without rows has two
+  // of zeros.)
+  auto steps_of = [&](const Tile& x) {
+    if constexpr (WEIGHTS) {
+      int64_t lo, hi;
+      group_rows(a, x.g, lo, hi);
+      return max(2, (int)((hi - lo + 63) / 64) * 2);
+    } else {
+      return (K + 2 * S::kStep - 1) / (2 * S::kStep) * 2;
+    }
+  };
+
+  // ---- producer: the stream of loads
+  const uint32_t chunk = (uint32_t)((lane & 3) ^ chunk_order(lane >> 4)) * 16;
+  const uint32_t lane_off_a = WEIGHTS ? strided_source<BM>(wave, lane, (uint32_t)K) : (uint32_t)(lane >> 2) * K + chunk;
+  const uint32_t lane_off_w = strided_source<BN>(wave, lane, (uint32_t)a.width * 2);
+  int p_tile = slot, p_step = 0, p_steps = 0, p_stage = 0;
+  __amdgpu_buffer_rsrc_t ra, rw;
+  Strided sa{}, sw{};
+  auto next_tile = [&]() {
+    const bool any = p_tile < total;
+    const Tile x = tile(any ? p_tile : slot);
+    const int64_t row = (int64_t)a.width * 2;
+    p_steps = steps_of(x);
+    if constexpr (WEIGHTS) {
+      int64_t lo, hi;
+      group_rows(a, x.g, lo, hi);
+      const int64_t n = any ? hi - lo : 0;
+      sa.start(a.a + lo * K + x.m0 * 2, n, K, K - x.m0 * 2);
+      sw.start(a.w + lo * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
+    } else {
+      ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
+      sw.start(a.w + (int64_t)x.g * a.N * row + (int64_t)x.c0 * 2, any ? a.N : 0, row, row - (int64_t)x.c0 * 2);
+    }
+    p_tile += gridDim.x;
+    p_step = 0;
+  };
+  // descriptors of the stream's next step
+  auto describe = [&]() {
+    if (p_step == p_steps) next_tile();
+    if constexpr (WEIGHTS) ra = sa.step();
+    rw = sw.step();
+  };
+  // load i of this wave's kLoads for the next step of the stream
+  auto load_one = [&](int i) {
+    uint8_t* st = tile_lds + p_stage * S::kStage;
+    if (i < S::kLoadsA) {
+      const int at = (i * S::kWaves + wave) * 1024;
+      uint32_t off = lane_off_a;
+      asm("" : "+v"(off));  // one register and an addition a load, rather than a register a load
+      if constexpr (WEIGHTS) {
+        // 1 KiB is 512 / BM indexes
+        load16_to_lds(ra, st + at, off + (uint32_t)(i * S::kWaves * (512 / BM)) * K);
+      } else {
+        const uint32_t k0 = (uint32_t)p_step * S::kStep;
+        off += k0 + (uint32_t)((i * S::kWaves + wave) * 16) * K;
+        load16_to_lds(ra, st + at, k0 + chunk < (uint32_t)K ? off : kBeyond);
+      }
+    } else {
+      const int j = i - S::kLoadsA;
+      uint32_t off = lane_off_w;
+      asm("" : "+v"(off));
+      load16_to_lds(rw, st + kImageA + (j * S::kWaves + wave) * 1024,
+                    off + (uint32_t)(j * S::kWaves * (512 / BN) * 2) * a.width);
+    }
+  };
+  auto advance = [&]() {
+    ++p_step;
+    p_stage = (p_stage + 1) % S::kStages;
+  };
+
+  // ---- consumer
+  auto row_of = [](int m) { return m < MT / 2 ? m * 16 : (m - MT / 2) * 16 + BM / 2; };  // row tile m of wave row 0
+  const int frag = r * S::kStep + ((q ^ chunk_order(r >> 2)) * 16);
+  uint32_t a_at[4], w_at[NT];
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+    a_at[m] = WEIGHTS ? strided_frag<BM>(lane, (wm * (MT / 2) * 16 + row_of(m)) / 16)
+                      : (uint32_t)((wm * (MT / 2) * 16 + row_of(m)) * S::kStep + frag);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) w_at[n] = kImageA + strided_frag<BN>(lane, wn * NT + n);
+  uint32_t pair = 0;  // 0 or kPair: the current pair of stages
+  acc_t acc[MT][NT];
+  i32x4 av[4], wv[2][NT];
+  auto read_a = [&](uint32_t stage, int m) {
+    // (row tiles 4..7 of 256 rows: eight blocks, or 128 rows, on)
+    const uint8_t* at = tile_lds + stage + a_at[m % 4] + (m / 4) * (WEIGHTS ? 8 * 32 : 128 * S::kStep);
+    if constexpr (WEIGHTS)
+      return read_strided<BM>(at);
+    else
+      return *(const i32x4*)at;
+  };
+  auto read_w = [&](uint32_t stage, int n) { return read_strided<BN>(tile_lds + stage + w_at[n]); };
+  // One step; h: its place in the pair.
+  auto step = [&](auto hc, auto mtn) {
+    constexpr int h = decltype(hc)::value, MTN = decltype(mtn)::value;
+    step_sync<S::kLoads>();
+    describe();
+    const uint32_t here = pair + h * S::kStage, next = h ? kPair - pair : pair + S::kStage;
+#pragma unroll
+    for (int u = 0; u < MTN; ++u) {
+      constexpr int kW0 = MTN > 4 ? 2 : 0;  // the next step's column fragments: units kW0..kW0 + NT - 1
+      av[(u + 3) % 4] = u + 3 < MTN ? read_a(here, u + 3) : read_a(next, u + 3 - MTN);
+      if (u >= kW0 && u < kW0 + NT) wv[1 - h][u - kW0] = read_w(next, u - kW0);
+#pragma unroll
+      for (int i = u; i < S::kLoads; i += MTN) load_one(i);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[u][n] = AR::mfma(wv[h][n], av[u % 4], acc[u][n]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    advance();
+  };
+
+  // the first three steps of the stream, and the first fragments
+  for (int s = 0; s < 3; ++s) {
+    describe();
+    for (int i = 0; i < S::kLoads; ++i) load_one(i);
+    advance();
+  }
+  step_sync<2 * S::kLoads>();
+#pragma unroll
+  for (int n = 0; n < NT; ++n) wv[0][n] = read_w(0, n);
+#pragma unroll
+  for (int u = 0; u < 3; ++u) av[u] = read_a(0, u);
+
+  for (int t = slot; t < total; t += gridDim.x) {
+    const Tile x = tile(t);
+    const int steps = steps_of(x);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = acc_t{0, 0, 0, 0};
+    auto run = [&](auto mtn) {
+      for (int s = 0; s < steps; s += 2) {
+        step(std::integral_constant<int, 0>{}, mtn);
+        step(std::integral_constant<int, 1>{}, mtn);
+        pair = kPair - pair;
+      }
+    };
+    if (!HALVES || x.rows > BM / 2)
+      run(std::integral_constant<int, MT>{});
+    else
+      run(std::integral_constant<int, HALVES ? MT / 2 : MT>{});
+
+    // epilogue: lane (q, r) has columns 4 q.. of row r of each 16 x 16; of two column
+    // tiles odd q's of the first and even q's of the second trade places
+    int er = r, eq = q;
+    asm volatile("" : "+v"(er), "+v"(eq));  // what follows is not kept in registers over the steps
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = wm * (MT / 2) * 16 + row_of(m) + er;
+      const int64_t at = ((WEIGHTS ? (int64_t)x.g * a.N : 0) + x.m0 + row) * a.width;
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[m][n][i]), __float_as_uint(acc[m][n + 1][i]),
+                                                          false, false);
+          v[i] = __uint_as_float(s[0]);
+          v[4 + i] = __uint_as_float(s[1]);
+        }
+        const int col = x.c0 + wn * S::CW + (n + (eq & 1)) * 16 + (eq >> 1) * 8;
+        if (row < x.rows) store_cols<IO, 8>(a.out, at + col, col, x.c0 + x.cols, v);
+      }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+}
+
+// Gradient of the gate: with out = silu(g) u,
+//   dg = grad u s (1 + g (1 - s)),  du = grad g s,  s = 1 / (1 + exp(-g)).
+// Rounded to the rows' type, as the products' operands have to be; their sums are fp32.
+// Bound by memory.
+template <typename IO>
+__global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restrict__ pre, const void* __restrict__ grad,
+                                                            int64_t pieces, int width, void* __restrict__ out) {
+  typedef typename IO::type T;
+  const int per = width / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per;
+    const int64_t at = row * 2 * width + (i - row * per) * 8;
+    float g[8], u[8], d[8], dg[8], du[8];
+    IO::unpack(__builtin_nontemporal_load((const typename IO::piece*)((const T*)pre + at)), g);
+    IO::unpack(__builtin_nontemporal_load((const typename IO::piece*)((const T*)pre + at + width)), u);
+    IO::unpack(__builtin_nontemporal_load((const typename IO::piece*)((const T*)grad + i * 8)), d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // (an infinite exponential gives s = 0, and g s its limit 0 for finite g)
+      const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g[j]));
+      du[j] = d[j] * g[j] * s;
+      dg[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+    }
+    IO::store_piece((T*)out + at, dg);
+    IO::store_piece((T*)out + at + width, du);
+  }
+}
+
+}  // namespace ep
