@@ -63,8 +63,10 @@ __device__ __forceinline__ uint32_t strided_frag(int lane, int block) {
   return (uint32_t)(q * 8 + (i >> 2)) * (WIDTH * 2) + (uint32_t)(block ^ f) * 32 + (i & 3) * 8;
 }
 
+// (`__restrict__` gives the reads alias information; without any the compiler waits for all
+// direct loads to LDS in flight before each of them: 4.44 against 2.1 ms for 65536 rows of 32 experts, 4096 x 4096.)
 template <int WIDTH>
-__device__ __forceinline__ i32x4 read_strided(const uint8_t* at) {
+__device__ __forceinline__ i32x4 read_strided(const uint8_t* __restrict__ at) {
   typedef short i16x4 __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
   typedef int i32x2 __attribute__((ext_vector_type(2)));
