@@ -211,7 +211,7 @@ def lib() -> ctypes.CDLL:
         L.ep_rms_norm_backward.argtypes = [i32, vp, i64, vp, i32, f32, vp, i64, vp, i64, i64, i32, vp, vp, vp, vp]
         L.ep_matmul_fp8.argtypes = [vp, vp, i64, vp, vp, i32, vp, vp, i32, i32, u32, i32, vp, vp]
         L.ep_matmul.argtypes = [i32, vp, i64, vp, i32, vp, vp, i32, i32, u32, vp, vp, vp]
-        L.ep_matmul_backward_workspace.argtypes = [i64, i32, u32, ctypes.POINTER(i64)]
+        L.ep_matmul_backward_workspace.argtypes = [i64, i32, i32, i32, u32, ctypes.POINTER(i64)]
         L.ep_matmul_backward.argtypes = [i32, vp, i64, vp, vp, vp, i32, vp, vp, i32, i32, u32, vp, vp, i32, vp, vp]
         for fn in ("ep_matmul_fp8", "ep_matmul", "ep_matmul_backward_workspace", "ep_matmul_backward", "ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
             getattr(L, fn).restype = i32
@@ -1075,13 +1075,12 @@ def matmul_backward(a, w, grad, rows=None, gated: bool = False, pre=None, out=No
             if gw.dtype == torch.float32:
                 gcode = 0
             _require(gw, torch.float32 if gcode == 0 else dtype, w.shape, "grad_w", device)
-    space = None
-    if gated:
-        size = ctypes.c_int64()
-        _check(lib().ep_matmul_backward_workspace(M, N, _GATED, ctypes.byref(size)))
-        space = torch.empty(size.value, dtype=torch.uint8, device=device)
+    flags = _GATED if gated else 0
+    size = ctypes.c_int64()
+    _check(lib().ep_matmul_backward_workspace(M, G, K, N, flags, ctypes.byref(size)))
+    space = torch.empty(size.value, dtype=torch.uint8, device=device) if size.value else None
     _launch(device, lib().ep_matmul_backward, code, a.data_ptr(), M, w.data_ptr(), grad.data_ptr(), _ptr(pre), G,
-            _ptr(start), _ptr(count), K, N, _GATED if gated else 0, _ptr(ga), _ptr(gw), gcode, _ptr(space))
+            _ptr(start), _ptr(count), K, N, flags, _ptr(ga), _ptr(gw), gcode, _ptr(space))
     return ga, gw
 
 

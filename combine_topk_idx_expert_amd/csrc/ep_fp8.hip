@@ -23,7 +23,7 @@ extern "C" ep_status ep_matmul_fp8(const uint8_t* a, const float* a_scale, int64
   const bool cols = flags & EP_FP8_SCALES_COL_MAJOR;
   MatmulArgs m{a, a_scale, w, w_scale, num_groups > 0 ? row_start : nullptr, num_groups > 0 ? row_count : nullptr,
                out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer, 0, num_rows, nullptr,
-               cols ? 1 : (inner + 127) / 128, cols ? num_rows : 1};
+               cols ? 1 : (inner + 127) / 128, cols ? num_rows : 1, 1};
   return with_type(out_type, [&](auto io) {
     typedef std::conditional_t<std::is_same_v<decltype(io), F32>, Fp8ExactMath, Fp8Math> AR;
     return gated ? launch_matmul<AR, decltype(io), true>(m, (hipStream_t)stream)

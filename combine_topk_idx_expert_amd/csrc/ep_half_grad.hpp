@@ -75,6 +75,10 @@ __device__ __forceinline__ i32x4 read_strided(const uint8_t* __restrict__ at) {
   return i32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
+// Where tiles are few and the inner dimension long, each is computed by several workgroups,
+// a slice of the inner dimension each, into fp32 results that join_slices_kernel adds in a
+// fixed order.
+//
 // MatmulArgs here: a = d [M][N], K its row's bytes; w = the weights [G][N][width], or for
 // the weights' gradient the rows a [M][width]; out = [M][width] or [G][N][width].
 //
@@ -111,13 +115,14 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
   const int q = lane >> 4, r = lane & 15;
 
   const int m_tiles = (a.N + BM - 1) / BM;
-  int total;
+  int each;  // tiles of a slice
   if constexpr (WEIGHTS) {
-    total = a.G * m_tiles * n_tiles;
+    each = a.G * m_tiles * n_tiles;
   } else {
     tile_starts<S::kThreads, BM>(a, pre);
-    total = uniform(pre[a.G]) * n_tiles;
+    each = uniform(pre[a.G]) * n_tiles;
   }
+  const int total = each * a.slices;
   const int K = a.K;
   const int per = gridDim.x / 8;
   const int slot = gridDim.x % 8 == 0 ? ((int)blockIdx.x % 8) * per + (int)blockIdx.x / 8 : (int)blockIdx.x;
@@ -125,21 +130,23 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
 
   auto tile = [&](int t) {
     if constexpr (WEIGHTS)
-      return locate_weights<BM, BN>(a, m_tiles, n_tiles, t);
+      return locate_weights<BM, BN>(a, m_tiles, n_tiles, t % each);
     else
-      return locate<BM, BN>(a, pre, n_tiles, t);
+      return locate<BM, BN>(a, pre, n_tiles, t % each);
   };
-  // steps of a tile, even: stages and registers take turns.  (A group without rows has two
-  // of zeros.)
-  auto steps_of = [&](const Tile& x) {
-    if constexpr (WEIGHTS) {
-      int64_t lo, hi;
-      group_rows(a, x.g, lo, hi);
-      return max(2, (int)((hi - lo + 63) / 64) * 2);
-    } else {
-      return (K + 2 * S::kStep - 1) / (2 * S::kStep) * 2;
+  // Inner indexes [lo, hi) of tile t: the group's rows or the channels, or a slice of them.
+  auto inner = [&](int t, const Tile& x, int64_t& lo, int64_t& hi) {
+    lo = 0;
+    hi = a.N;
+    if constexpr (WEIGHTS) group_rows(a, x.g, lo, hi);
+    if (a.slices > 1) {
+      const int64_t len = ((hi - lo + a.slices - 1) / a.slices + 63) / 64 * 64;
+      lo = min(hi, lo + t / each * len);
+      hi = min(hi, lo + len);
     }
   };
+  // steps of a tile, even: stages and registers take turns.  (Without indexes two of zeros.)
+  auto steps_of = [&](int64_t lo, int64_t hi) { return max(2, (int)((hi - lo + 63) / 64) * 2); };
 
   // ---- producer: the stream of loads
   const uint32_t chunk = (uint32_t)((lane & 3) ^ chunk_order(lane >> 4)) * 16;
@@ -148,20 +155,24 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
   int p_tile = slot, p_step = 0, p_steps = 0, p_stage = 0;
   __amdgpu_buffer_rsrc_t ra, rw;
   Strided sa{}, sw{};
+  uint32_t a_from = 0, a_to = 0;  // rows' gradient: the bytes of d's rows that the tile needs
   auto next_tile = [&]() {
     const bool any = p_tile < total;
-    const Tile x = tile(any ? p_tile : slot);
+    const int t = any ? p_tile : slot;
+    const Tile x = tile(t);
     const int64_t row = (int64_t)a.width * 2;
-    p_steps = steps_of(x);
+    int64_t lo, hi;
+    inner(t, x, lo, hi);
+    p_steps = steps_of(lo, hi);
+    const int64_t n = any ? hi - lo : 0;
     if constexpr (WEIGHTS) {
-      int64_t lo, hi;
-      group_rows(a, x.g, lo, hi);
-      const int64_t n = any ? hi - lo : 0;
       sa.start(a.a + lo * K + x.m0 * 2, n, K, K - x.m0 * 2);
       sw.start(a.w + lo * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
     } else {
       ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
-      sw.start(a.w + (int64_t)x.g * a.N * row + (int64_t)x.c0 * 2, any ? a.N : 0, row, row - (int64_t)x.c0 * 2);
+      a_from = (uint32_t)lo * 2;
+      a_to = (uint32_t)hi * 2;
+      sw.start(a.w + ((int64_t)x.g * a.N + lo) * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
     }
     p_tile += gridDim.x;
     p_step = 0;
@@ -183,9 +194,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
         // 1 KiB is 512 / BM indexes
         load16_to_lds(ra, st + at, off + (uint32_t)(i * S::kWaves * (512 / BM)) * K);
       } else {
-        const uint32_t k0 = (uint32_t)p_step * S::kStep;
+        const uint32_t k0 = a_from + (uint32_t)p_step * S::kStep;
         off += k0 + (uint32_t)((i * S::kWaves + wave) * 16) * K;
-        load16_to_lds(ra, st + at, k0 + chunk < (uint32_t)K ? off : kBeyond);
+        load16_to_lds(ra, st + at, k0 + chunk < a_to ? off : kBeyond);
       }
     } else {
       const int j = i - S::kLoadsA;
@@ -256,7 +267,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
 
   for (int t = slot; t < total; t += gridDim.x) {
     const Tile x = tile(t);
-    const int steps = steps_of(x);
+    int64_t lo, hi;
+    inner(t, x, lo, hi);
+    const int steps = steps_of(lo, hi);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -280,7 +293,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = wm * (MT / 2) * 16 + row_of(m) + er;
-      const int64_t at = ((WEIGHTS ? (int64_t)x.g * a.N : 0) + x.m0 + row) * a.width;
+      const int64_t first = WEIGHTS ? ((int64_t)(t / each) * a.G + x.g) * a.N : (int64_t)(t / each) * a.M;
+      const int64_t at = (first + x.m0 + row) * a.width;
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         float v[8];
@@ -297,6 +311,31 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+}
+
+// The sum of the slices' results (parts: [slices] of the whole) for the rows of each group;
+// the weights' gradient is one group of all its rows.  width is a multiple of 8.
+template <typename IO>
+__global__ __launch_bounds__(256) void join_slices_kernel(MatmulArgs a, const float* __restrict__ parts) {
+  const int col = ((int)blockIdx.x * 64 + (int)threadIdx.x % 64) * 8;
+  if (col >= a.width) return;
+  int64_t lo, hi;
+  group_rows(a, blockIdx.z, lo, hi);
+  for (int64_t row = lo + blockIdx.y * 4 + threadIdx.x / 64; row < hi; row += (int64_t)gridDim.y * 4) {
+    const int64_t at = row * a.width + col;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    for (int k = 0; k < a.slices; ++k) {
+      const float* p = parts + (int64_t)k * a.M * a.width + at;
+      float f[8];
+      F32::unpack(*(const F32::piece*)p, f);
+      F32::unpack(*(const F32::piece*)(p + 4), f + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += f[j];
+    }
+    IO::store8(a.out, at, v);
+  }
 }
 
 // Gradient of the gate: with out = silu(g) u,

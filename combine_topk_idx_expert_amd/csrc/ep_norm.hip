@@ -33,75 +33,79 @@ ep_status validate_norm(int32_t type, int64_t num_rows, int32_t num_cols, int32_
   return EP_OK;
 }
 
-template <typename IO, int W, int NC>
+template <typename IO, int L, int NC>
 ep_status launch_norm(const NormArgs& a, hipStream_t s) {
-  const int64_t blocks = W == 1 ? (a.N + 3) / 4 : a.N;
-  norm_kernel<IO, W, NC><<<(unsigned)blocks, W == 1 ? 256 : W * kWave, 0, s>>>(a);
+  constexpr int kRows = L <= kWave ? 256 / L : 1;
+  norm_kernel<IO, L, NC><<<(unsigned)((a.N + kRows - 1) / kRows), L <= kWave ? 256 : L, 0, s>>>(a);
   EP_LAUNCHED("norm_kernel");
   return EP_OK;
 }
 
-// A wave a row where there are rows for all CUs and a lane holds at most eight pieces:
-// no barrier.  Few or longer rows take four waves, the longest sixteen.
+// Lanes of a row: 16, 32 or 64 (no barrier) where they hold it in one piece each, 64 with two
+// pieces where there are rows for all CUs; else four waves, and sixteen for the longest.
+// (32768 rows of 4096 bf16: four waves of two pieces 201 us, a wave of eight 475.)
 template <typename IO>
 ep_status launch_norm(const NormArgs& a, hipStream_t s) {
   constexpr int V = 16 / sizeof(typename IO::type);
   const int pieces = (a.H + V - 1) / V;
-  if (a.N >= 4 * kCUs && pieces <= 8 * kWave) {
-    if (pieces <= kWave) return launch_norm<IO, 1, 1>(a, s);
-    if (pieces <= 2 * kWave) return launch_norm<IO, 1, 2>(a, s);
-    if (pieces <= 4 * kWave) return launch_norm<IO, 1, 4>(a, s);
-    return launch_norm<IO, 1, 8>(a, s);
-  }
-  if (pieces <= 4 * kWave) return launch_norm<IO, 4, 1>(a, s);
-  if (pieces <= 8 * kWave) return launch_norm<IO, 4, 2>(a, s);
-  if (pieces <= 16 * kWave) return launch_norm<IO, 4, 4>(a, s);
-  if (pieces <= 32 * kWave) return launch_norm<IO, 4, 8>(a, s);
-  if (pieces <= 64 * kWave) return launch_norm<IO, 16, 4>(a, s);
-  return launch_norm<IO, 16, 8>(a, s);
+  if (pieces <= 16) return launch_norm<IO, 16, 1>(a, s);
+  if (pieces <= 32) return launch_norm<IO, 32, 1>(a, s);
+  if (pieces <= 64) return launch_norm<IO, 64, 1>(a, s);
+  if (pieces <= 2 * 64 && a.N >= 4 * kCUs) return launch_norm<IO, 64, 2>(a, s);
+  if (pieces <= 128) return launch_norm<IO, 128, 1>(a, s);
+  if (pieces <= 256) return launch_norm<IO, 256, 1>(a, s);
+  if (pieces <= 2 * 256) return launch_norm<IO, 256, 2>(a, s);
+  if (pieces <= 4 * 256) return launch_norm<IO, 256, 4>(a, s);
+  if (pieces <= 2 * 1024) return launch_norm<IO, 1024, 2>(a, s);
+  if (pieces <= 4 * 1024) return launch_norm<IO, 1024, 4>(a, s);
+  if constexpr (V == 4) return launch_norm<IO, 1024, 8>(a, s);
+  return fail(EP_ERR_SHAPE, "rows too long");  // not reached: validate_rows bounds them
 }
 
-// Teams of the gradient: W waves that take a row, and how many of them.
+// The gradient's teams of lanes, pieces of a lane, and workgroups.
 struct NormTeams {
-  int waves, nc, teams;
+  int lanes, nc, groups;
 };
 
-// Rows of up to 64 pieces take a wave, longer ones 4, 8 or 16 waves with at most four
-// (fp32: eight) pieces a lane.  Every team writes a row of fp32 sums, so there are
-// no more teams than fill the card, and for few rows one for every four.
+// Every workgroup writes a row of fp32 sums, so there are no more than fill the card, and for
+// few rows one for every four.
 NormTeams norm_teams(int32_t type, int64_t N, int32_t H) {
   const int v = 16 / (int)type_bytes(type);
   const int pieces = (H + v - 1) / v;
-  NormTeams t{};
-  if (pieces <= kWave) t.waves = 1, t.nc = 1;
-  else if (pieces <= 4 * kWave) t.waves = 4, t.nc = 1;
-  else if (pieces <= 8 * kWave) t.waves = 4, t.nc = 2;
-  else if (pieces <= 16 * kWave) t.waves = 4, t.nc = 4;
-  else if (pieces <= 32 * kWave) t.waves = 8, t.nc = 4;
-  else if (pieces <= 64 * kWave) t.waves = 16, t.nc = 4;
-  else t.waves = 16, t.nc = 8;
-  const int64_t full = (int64_t)kCUs * (t.waves == 1 ? 16 : t.waves <= 4 ? 5 : 16 / t.waves);
-  t.teams = (int)std::min(full, std::max<int64_t>(std::min<int64_t>(N, kCUs), N / 4));
+  NormTeams t{1024, 1, 0};
+  if (pieces <= 16) t.lanes = 16;
+  else if (pieces <= 32) t.lanes = 32;
+  else if (pieces <= 64) t.lanes = 64;
+  else if (pieces <= 128) t.lanes = 128;
+  else if (pieces <= 256) t.lanes = 256;
+  else if (pieces <= 512) t.lanes = 512;
+  else while (t.nc * 1024 < pieces) t.nc *= 2;
+  const int64_t full = kCUs * (t.lanes == 1024 ? 1 : t.lanes == 512 ? 2 : t.lanes == 128 ? 10 : 5);
+  const int64_t rows = t.lanes <= kWave ? 256 / t.lanes : 1;  // at once in a workgroup
+  const int64_t all = (N + rows - 1) / rows;
+  t.groups = (int)std::min(full, std::max<int64_t>(std::min<int64_t>(all, kCUs), all / 4));
   return t;
 }
 
-template <typename IO, int W, int NC>
+template <typename IO, int L, int NC>
 ep_status launch_norm_backward(const NormBwdArgs& a, hipStream_t s) {
-  const int blocks = W == 1 ? (a.teams + 3) / 4 : a.teams;
-  norm_backward_kernel<IO, W, NC><<<blocks, W == 1 ? 256 : W * kWave, 0, s>>>(a);
+  norm_backward_kernel<IO, L, NC><<<a.groups, L <= kWave ? 256 : L, 0, s>>>(a);
   EP_LAUNCHED("norm_backward_kernel");
   return EP_OK;
 }
 
 template <typename IO>
 ep_status launch_norm_backward(const NormBwdArgs& a, const NormTeams& t, hipStream_t s) {
-  if (t.waves == 1) return launch_norm_backward<IO, 1, 1>(a, s);
-  if (t.waves == 4 && t.nc == 1) return launch_norm_backward<IO, 4, 1>(a, s);
-  if (t.waves == 4 && t.nc == 2) return launch_norm_backward<IO, 4, 2>(a, s);
-  if (t.waves == 4) return launch_norm_backward<IO, 4, 4>(a, s);
-  if (t.waves == 8) return launch_norm_backward<IO, 8, 4>(a, s);
-  if (t.nc == 4) return launch_norm_backward<IO, 16, 4>(a, s);
-  if constexpr (sizeof(typename IO::type) == 4) return launch_norm_backward<IO, 16, 8>(a, s);
+  if (t.lanes == 16) return launch_norm_backward<IO, 16, 1>(a, s);
+  if (t.lanes == 32) return launch_norm_backward<IO, 32, 1>(a, s);
+  if (t.lanes == 64) return launch_norm_backward<IO, 64, 1>(a, s);
+  if (t.lanes == 128) return launch_norm_backward<IO, 128, 1>(a, s);
+  if (t.lanes == 256) return launch_norm_backward<IO, 256, 1>(a, s);
+  if (t.lanes == 512) return launch_norm_backward<IO, 512, 1>(a, s);
+  if (t.nc == 1) return launch_norm_backward<IO, 1024, 1>(a, s);
+  if (t.nc == 2) return launch_norm_backward<IO, 1024, 2>(a, s);
+  if (t.nc == 4) return launch_norm_backward<IO, 1024, 4>(a, s);
+  if constexpr (sizeof(typename IO::type) == 4) return launch_norm_backward<IO, 1024, 8>(a, s);
   return fail(EP_ERR_SHAPE, "rows too long");  // not reached: validate_rows bounds them
 }
 
@@ -123,9 +127,12 @@ ep_status ep_quantize_fp8(int32_t type, const void* x, int64_t num_rows, int32_t
     return fail(EP_ERR_SHAPE, "x / scales must be aligned to their element size");
   const bool cols = flags & EP_FP8_SCALES_COL_MAJOR;
   QuantFp8Args a{x, row_stride, codes, scales, cols ? 1 : nb, cols ? num_rows : 1, (uint32_t)num_rows, num_cols,
-                 (uint32_t)nb};
-  const unsigned blocks = (unsigned)((num_rows * nb + 15) / 16);
+                 (uint32_t)nb, 0, 31};
+  while ((int64_t)1 << (a.shift - 31) < nb) ++a.shift;
+  a.magic = (uint32_t)((((uint64_t)1 << a.shift) + nb - 1) / nb);
   return with_type(type, [&](auto io) -> ep_status {
+    constexpr int kEach = 16 * kQuantBlocks<decltype(io)>;
+    const unsigned blocks = (unsigned)((num_rows * nb + kEach - 1) / kEach);
     quantize_fp8_kernel<decltype(io)><<<blocks, 256, 0, (hipStream_t)stream>>>(a);
     EP_LAUNCHED("quantize_fp8_kernel");
     return EP_OK;
@@ -156,7 +163,7 @@ ep_status ep_rms_norm_backward_workspace(int32_t type, int64_t num_rows, int32_t
   if (!bytes) return fail(EP_ERR_NULL, "bytes is NULL");
   const ep_status st = validate_rows(type, num_rows, num_cols, EP_MAX_NORM_COLS);
   if (st != EP_OK) return st;
-  *bytes = (int64_t)norm_teams(type, num_rows, num_cols).teams * num_cols * (int64_t)sizeof(float);
+  *bytes = (int64_t)norm_teams(type, num_rows, num_cols).groups * num_cols * (int64_t)sizeof(float);
   return EP_OK;
 }
 
@@ -182,11 +189,11 @@ ep_status ep_rms_norm_backward(int32_t type, const void* x, int64_t x_stride, co
         misaligned(grad_total, b) || misaligned(grad_x, b) || misaligned(workspace, 4))
       return fail(EP_ERR_SHAPE, "every array must be aligned to its element size");
     NormBwdArgs a{x, weight, grad, grad_total, grad_x, (float*)workspace, x_stride, grad_stride, grad_total_stride,
-                  num_rows, t.teams, num_cols, weight_type == EP_TYPE_F32, eps};
+                  num_rows, t.groups, num_cols, weight_type == EP_TYPE_F32, eps};
     st = with_type(type, [&](auto io) { return launch_norm_backward<decltype(io)>(a, t, s); });
     if (st != EP_OK) return st;
   }
-  norm_weight_kernel<<<(num_cols + 31) / 32, 1024, 0, s>>>((const float*)workspace, t.teams, num_cols, grad_weight);
+  norm_weight_kernel<<<(num_cols + 31) / 32, 1024, 0, s>>>((const float*)workspace, t.groups, num_cols, grad_weight);
   EP_LAUNCHED("norm_weight_kernel");
   return EP_OK;
 }

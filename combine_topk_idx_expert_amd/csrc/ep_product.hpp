@@ -106,6 +106,7 @@ struct MatmulArgs {
   int64_t least, most;       // groups of other sizes are not this launch's
   void* pre;                 // gated, 16-bit: [M][N], the product before the gate; or null
   int64_t a_row_step, a_block_step;  // block b of row r has scale a_scale[r * a_row_step + b * a_block_step]
+  int slices;                // gradients: parts of the inner dimension, each with an out of its own; else 1
 };
 
 // Blocks of 128 channels of the weights: gated, each half has blocks of its own.

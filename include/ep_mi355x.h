@@ -545,14 +545,15 @@ ep_status ep_matmul(int32_t type, const void *a, int64_t num_rows, const void *w
  *                0) of grad_w_type (`type` or fp32), or NULL; zeros for a group
  *                without rows.
  *   workspace    device, 16-byte aligned, of the size that
- *                ep_matmul_backward_workspace gives for these sizes; free again when
- *                the call's work is done.
+ *                ep_matmul_backward_workspace gives for these sizes (NULL where that
+ *                is 0); free again when the call's work is done.
  * With d the gradient of the product (gated: through the gate, rounded to `type`, since
  * it is an operand of the next two): grad_a = d w, grad_w[g] = sum over the group's
  * rows of d[r] a[r], both summed in fp32 and rounded once.  inner is a multiple of 8,
  * outer of 8, gated of 16.  The tensors are 16-byte aligned.
  * Errors as ep_matmul. */
-ep_status ep_matmul_backward_workspace(int64_t num_rows, int32_t outer, uint32_t flags, int64_t *bytes);
+ep_status ep_matmul_backward_workspace(int64_t num_rows, int32_t num_groups, int32_t inner, int32_t outer,
+                                       uint32_t flags, int64_t *bytes);
 ep_status ep_matmul_backward(int32_t type, const void *a, int64_t num_rows, const void *w, const void *grad,
                              const void *pre, int32_t num_groups, const int64_t *row_start, const int32_t *row_count,
                              int32_t inner, int32_t outer, uint32_t flags, void *grad_a, void *grad_w,
