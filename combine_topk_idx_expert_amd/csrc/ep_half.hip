@@ -82,12 +82,12 @@ int64_t slice_bytes(const GradPlan& p, int64_t rows, int width) {
 
 template <typename AR, typename IO, bool WEIGHTS, int BM, bool HALVES>
 ep_status launch_half_grad(const MatmulArgs& a, const GradPlan& p, hipStream_t s) {
-  typedef TileShape<BM, 256, 2, 4> S;
+  typedef Tile128Shape<BM, 256, 2, 4, false> S;
   const int64_t most = p.most * a.slices;
   if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "gradient of %lld tiles is too large", (long long)most);
   const int grid = (int)std::min<int64_t>(most, kCUs);
   half_grad_kernel<AR, IO, WEIGHTS, BM, 256, 2, 4, HALVES>
-      <<<grid, S::kThreads, S::lds(WEIGHTS ? 0 : a.G, false), s>>>(a, p.n_tiles);
+      <<<grid, S::kThreads, S::lds(WEIGHTS ? 0 : a.G), s>>>(a, p.n_tiles);
   EP_LAUNCHED("half_grad_kernel");
   return EP_OK;
 }

@@ -2,21 +2,22 @@
 // weights, in tiles staged through LDS; the gate's gradient.
 #pragma once
 
-#include "ep_product_tile.hpp"
+#include "ep_product_tile128.hpp"
 
 namespace ep {
 
 // y = a w^T has the gradients d w (of the rows; inner dimension: channels) and, for
 // each group, d^T a (of its weights; inner dimension: the group's rows).  The inner
 // dimension is not contiguous in w, and in neither operand of d^T a: their stages in
-// LDS are images of 32 inner indexes by BM or BN values, read with ds_read_b64_tr_b16.
+// LDS are images of 64 inner indexes by BM or BN values, read with ds_read_b64_tr_b16.
 // For 16 lanes that instruction takes four rows of 16 values (lane i: 8 bytes of row
 // i / 4, values 4 (i % 4)..) and gives lane i the four of column i, so two of them make
 // a lane's operand of the matrix instruction.
 //
-// Stream of steps, ring of four stages, order of tiles and halves as in
-// ep_product_tile.hpp, with one difference: a wave's column tiles are 16 neighbouring
+// Stream of steps, two stages, one barrier a step, order of tiles and halves as in
+// ep_product_tile128.hpp, with one difference: a wave's column tiles are 16 neighbouring
 // columns each, and v_permlane16_swap gives a lane eight neighbours of a row at the end.
+// (65536 rows of 32 experts, 4096 x 4096: rows XXR ms, weights XXW, RATE.)
 //
 // Image of a strided operand: index k has 512 (256) bytes, blocks of 32 bytes (16 values)
 // in the order block ^ f(k), f(k) = k % 4 + 4 (k / 8 % 2): the eight k whose blocks 32
@@ -35,10 +36,10 @@ struct Strided {
     tail = tail_;
   }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t step() {
-    const int64_t n = left < 32 ? left : 32;
+    const int64_t n = left < 64 ? left : 64;
     const __amdgpu_buffer_rsrc_t r = buffer_of(at, n > 0 ? (n - 1) * stride + tail : 0);
-    at += 32 * stride;
-    left -= 32;
+    at += 64 * stride;
+    left -= 64;
     return r;
   }
 };
@@ -55,7 +56,7 @@ __device__ __forceinline__ uint32_t strided_source(int wave, int lane, uint32_t 
 }
 
 // The byte of the image that lane reads for block `block`: index q * 8 + i / 4, the
-// second half of its operand four indexes on.
+// second half of its operand four indexes on, the step's second half 32 indexes on.
 template <int WIDTH>
 __device__ __forceinline__ uint32_t strided_frag(int lane, int block) {
   const int q = lane >> 4, i = lane & 15;
@@ -101,14 +102,13 @@ __device__ __forceinline__ Tile locate_weights(const MatmulArgs& a, int m_tiles,
 
 template <typename AR, typename IO, bool WEIGHTS, int BM, int BN, int WM, int WN, bool HALVES>
 __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, int n_tiles) {
-  typedef TileShape<BM, BN, WM, WN> S;
+  typedef Tile128Shape<BM, BN, WM, WN, false> S;
   constexpr int MT = S::MT, NT = S::NT;
-  constexpr int kPair = 2 * S::kStage;  // the stages of an even and the next odd step
-  constexpr int kImageA = BM * S::kStep;
-  static_assert(MT % 4 == 0 && NT == 4 && BN == 256 && (BM == 256 || BM == 128), "fragment rings and images");
-  typedef typename AR::acc acc_t;
+  constexpr int kImageA = BM * S::kRowBytes;
+  static_assert(MT % 4 == 0 && NT == 4 && BN == 256 && (BM == 256 || BM == 128), "fragment registers and images");
+  typedef typename AR::frag frag_t;
   extern __shared__ uint8_t tile_lds[];
-  int* const pre = (int*)(tile_lds + S::kStages * S::kStage);
+  int* const pre = (int*)(tile_lds + 2 * S::kStage);
   const int lane = lane_id();
   const int wave = uniform((int)threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
@@ -145,14 +145,15 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
       hi = min(hi, lo + len);
     }
   };
-  // steps of a tile, even: stages and registers take turns.  (Without indexes two of zeros.)
-  auto steps_of = [&](int64_t lo, int64_t hi) { return max(2, (int)((hi - lo + 63) / 64) * 2); };
+  // steps of a tile (without indexes one of zeros)
+  auto steps_of = [&](int64_t lo, int64_t hi) { return max(1, (int)((hi - lo + 63) / 64)); };
 
   // ---- producer: the stream of loads
-  const uint32_t chunk = (uint32_t)((lane & 3) ^ chunk_order(lane >> 4)) * 16;
-  const uint32_t lane_off_a = WEIGHTS ? strided_source<BM>(wave, lane, (uint32_t)K) : (uint32_t)(lane >> 2) * K + chunk;
+  const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+  const uint32_t lane_off_a = WEIGHTS ? strided_source<BM>(wave, lane, (uint32_t)K) : (uint32_t)(lane >> 3) * K + chunk;
   const uint32_t lane_off_w = strided_source<BN>(wave, lane, (uint32_t)a.width * 2);
-  int p_tile = slot, p_step = 0, p_steps = 0, p_stage = 0;
+  int p_tile = slot, p_step = 0, p_steps = 0;
+  uint32_t p_stage = 0;
   __amdgpu_buffer_rsrc_t ra, rw;
   Strided sa{}, sw{};
   uint32_t a_from = 0, a_to = 0;  // rows' gradient: the bytes of d's rows that the tile needs
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
   };
   // load i of this wave's kLoads for the next step of the stream
   auto load_one = [&](int i) {
-    uint8_t* st = tile_lds + p_stage * S::kStage;
+    uint8_t* st = tile_lds + p_stage;
     if (i < S::kLoadsA) {
       const int at = (i * S::kWaves + wave) * 1024;
       uint32_t off = lane_off_a;
@@ -194,8 +195,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
         // 1 KiB is 512 / BM indexes
         load16_to_lds(ra, st + at, off + (uint32_t)(i * S::kWaves * (512 / BM)) * K);
       } else {
-        const uint32_t k0 = a_from + (uint32_t)p_step * S::kStep;
-        off += k0 + (uint32_t)((i * S::kWaves + wave) * 16) * K;
+        const uint32_t k0 = a_from + (uint32_t)p_step * S::kRowBytes;
+        off += k0 + (uint32_t)((i * S::kWaves + wave) * 8) * K;
         load16_to_lds(ra, st + at, k0 + chunk < a_to ? off : kBeyond);
       }
     } else {
@@ -208,62 +209,77 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
   };
   auto advance = [&]() {
     ++p_step;
-    p_stage = (p_stage + 1) % S::kStages;
+    p_stage ^= S::kStage;
   };
 
   // ---- consumer
   auto row_of = [](int m) { return m < MT / 2 ? m * 16 : (m - MT / 2) * 16 + BM / 2; };  // row tile m of wave row 0
-  const int frag = r * S::kStep + ((q ^ chunk_order(r >> 2)) * 16);
+  const uint32_t frag0 = r * S::kRowBytes + (q ^ (r & 7)) * 16, frag1 = frag0 ^ 64;  // of the two halves of a step
   uint32_t a_at[4], w_at[NT];
 #pragma unroll
   for (int m = 0; m < 4; ++m)
     a_at[m] = WEIGHTS ? strided_frag<BM>(lane, (wm * (MT / 2) * 16 + row_of(m)) / 16)
-                      : (uint32_t)((wm * (MT / 2) * 16 + row_of(m)) * S::kStep + frag);
+                      : (uint32_t)((wm * (MT / 2) * 16 + row_of(m)) * S::kRowBytes);
 #pragma unroll
   for (int n = 0; n < NT; ++n) w_at[n] = kImageA + strided_frag<BN>(lane, wn * NT + n);
-  uint32_t pair = 0;  // 0 or kPair: the current pair of stages
-  acc_t acc[MT][NT];
-  i32x4 av[4], wv[2][NT];
-  auto read_a = [&](uint32_t stage, int m) {
+  uint32_t cur = 0;  // the current stage
+  f32x4 acc[MT][NT];
+  frag_t av[2], wv[NT];
+  auto read_a = [&](uint32_t stage, int slot_, int m) {
     // (row tiles 4..7 of 256 rows: eight blocks, or 128 rows, on)
-    const uint8_t* at = tile_lds + stage + a_at[m % 4] + (m / 4) * (WEIGHTS ? 8 * 32 : 128 * S::kStep);
+    const uint8_t* at = tile_lds + stage + a_at[m % 4] + (m / 4) * (WEIGHTS ? 8 * 32 : 128 * S::kRowBytes);
     if constexpr (WEIGHTS)
-      return read_strided<BM>(at);
+      av[slot_] = AR::make(read_strided<BM>(at), read_strided<BM>(at + 32 * BM * 2));
     else
-      return *(const i32x4*)at;
+      av[slot_] = AR::make(*(const i32x4*)(at + frag0), *(const i32x4*)(at + frag1));
   };
-  auto read_w = [&](uint32_t stage, int n) { return read_strided<BN>(tile_lds + stage + w_at[n]); };
-  // One step; h: its place in the pair.
-  auto step = [&](auto hc, auto mtn) {
-    constexpr int h = decltype(hc)::value, MTN = decltype(mtn)::value;
-    step_sync<S::kLoads>();
+  auto w_half = [&](uint32_t stage, int n, int h) {
+    return read_strided<BN>(tile_lds + stage + w_at[n] + h * 32 * BN * 2);
+  };
+  // One step of MTN row tiles.
+  auto step = [&](auto mtn) {
+    constexpr int MTN = decltype(mtn)::value;
+    const uint32_t next = cur ^ S::kStage;
     describe();
-    const uint32_t here = pair + h * S::kStage, next = h ? kPair - pair : pair + S::kStage;
 #pragma unroll
     for (int u = 0; u < MTN; ++u) {
-      constexpr int kW0 = MTN > 4 ? 2 : 0;  // the next step's column fragments: units kW0..kW0 + NT - 1
-      av[(u + 3) % 4] = u + 3 < MTN ? read_a(here, u + 3) : read_a(next, u + 3 - MTN);
-      if (u >= kW0 && u < kW0 + NT) wv[1 - h][u - kW0] = read_w(next, u - kW0);
+      constexpr int kLast = MTN - 1;
+      if (u == kLast) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read_a(next, 0, 0);
 #pragma unroll
-      for (int i = u; i < S::kLoads; i += MTN) load_one(i);
+        for (int i = 0; i < S::kLoads; i += 2) load_one(i);
+      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[u][n] = AR::mfma(wv[h][n], av[u % 4], acc[u][n]);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[u][n] = AR::mfma(wv[n].v[h], av[u % 2].v[h], acc[u][n]);
+          if (u == kLast) wv[n].v[h] = w_half(next, n, h);
+        }
+      if (u + 2 < MTN) read_a(cur, u % 2, u + 2);
+      if (u == kLast) {
+        read_a(next, 1, 1);
+#pragma unroll
+        for (int i = 1; i < S::kLoads; i += 2) load_one(i);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     advance();
+    cur = next;
   };
 
-  // the first three steps of the stream, and the first fragments
-  for (int s = 0; s < 3; ++s) {
+  // the first two steps of the stream, and the first fragments
+  for (int s = 0; s < 2; ++s) {
     describe();
     for (int i = 0; i < S::kLoads; ++i) load_one(i);
     advance();
   }
-  step_sync<2 * S::kLoads>();
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kLoads) : "memory");
 #pragma unroll
-  for (int n = 0; n < NT; ++n) wv[0][n] = read_w(0, n);
-#pragma unroll
-  for (int u = 0; u < 3; ++u) av[u] = read_a(0, u);
+  for (int n = 0; n < NT; ++n) wv[n] = AR::make(w_half(0, n, 0), w_half(0, n, 1));
+  read_a(0, 0, 0);
+  read_a(0, 1, 1);
 
   for (int t = slot; t < total; t += gridDim.x) {
     const Tile x = tile(t);
@@ -273,13 +289,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = acc_t{0, 0, 0, 0};
+      for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto run = [&](auto mtn) {
-      for (int s = 0; s < steps; s += 2) {
-        step(std::integral_constant<int, 0>{}, mtn);
-        step(std::integral_constant<int, 1>{}, mtn);
-        pair = kPair - pair;
-      }
+      for (int s = 0; s < steps; ++s) step(mtn);
     };
     if (!HALVES || x.rows > BM / 2)
       run(std::integral_constant<int, MT>{});

@@ -31,6 +31,11 @@ struct Bf16Math {
   static __device__ __forceinline__ acc mfma(i32x4 w, i32x4 a, acc c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(operand, w), __builtin_bit_cast(operand, a), c, 0, 0, 0);
   }
+  // 128 bytes of the inner dimension
+  struct frag {
+    i32x4 v[2];
+  };
+  static __device__ __forceinline__ frag make(i32x4 lo, i32x4 hi) { return frag{{lo, hi}}; }
 };
 struct F16Math {
   typedef f32x4 acc;
@@ -39,6 +44,11 @@ struct F16Math {
   static __device__ __forceinline__ acc mfma(i32x4 w, i32x4 a, acc c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(operand, w), __builtin_bit_cast(operand, a), c, 0, 0, 0);
   }
+  // 128 bytes of the inner dimension
+  struct frag {
+    i32x4 v[2];
+  };
+  static __device__ __forceinline__ frag make(i32x4 lo, i32x4 hi) { return frag{{lo, hi}}; }
 };
 // E4M3 with a scale for each 128 channels of a row and 128 x 128 of a weight: the
 // products of a block are summed by the instruction, and scaled when they are added

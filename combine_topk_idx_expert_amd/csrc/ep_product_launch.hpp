@@ -3,10 +3,10 @@
 
 #include <algorithm>
 
-#include "ep_fp8_tile.hpp"
 #include "ep_host.hpp"
 #include "ep_product.hpp"
 #include "ep_product_tile.hpp"
+#include "ep_product_tile128.hpp"
 
 namespace ep {
 
@@ -30,10 +30,13 @@ ep_status launch_matmul_tile(const MatmulArgs& a, hipStream_t s) {
   const int64_t most = (a.M / BM + a.G) * n_tiles;  // each group's last row tile may be partly filled
   if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "product of %lld tiles is too large", (long long)most);
   const int grid = (int)std::min<int64_t>(most, kCUs);
-  if constexpr (AR::kScales == kBlockScales) {
-    typedef Fp8Shape<BM, BN, WM, WN> F;
-    fp8_tile_kernel<AR, IO, GATED, BM, BN, WM, WN, HALVES><<<grid, F::kThreads, F::lds(a.G), s>>>(a, (int)n_tiles);
-    EP_LAUNCHED("fp8_tile_kernel");
+#ifndef T128
+#define T128 (BM == 256 || AR::kScales == kBlockScales)
+#endif
+  if constexpr (AR::kScales != kRowScales && T128) {
+    typedef Tile128Shape<BM, BN, WM, WN, AR::kScales == kBlockScales> T;
+    matmul_tile128_kernel<AR, IO, GATED, BM, BN, WM, WN, HALVES><<<grid, T::kThreads, T::lds(a.G), s>>>(a, (int)n_tiles);
+    EP_LAUNCHED("matmul_tile128_kernel");
   } else {
     const size_t lds = S::lds(a.G, AR::kScales == kRowScales);
     matmul_tile_kernel<AR, IO, GATED, BM, BN, WM, WN, HALVES><<<grid, S::kThreads, lds, s>>>(a, (int)n_tiles);

@@ -1,5 +1,5 @@
-// ep_fp8_tile.hpp -- product of E4M3 rows with block scales in tiles staged
-// through LDS.
+// ep_product_tile128.hpp -- products of E4M3 rows with block scales and of 16-bit rows in
+// tiles staged through LDS, in steps of 128 bytes.
 #pragma once
 
 #include "ep_product_tile.hpp"
@@ -7,39 +7,46 @@
 namespace ep {
 
 // A workgroup of WM x WN waves computes tiles of BM rows x BN channels, one after the
-// other, in steps of a block of 128 channels of the inner dimension; the steps of all
-// its tiles form one stream, as in ep_product_tile.hpp.  A step is one matrix
-// instruction for each 16 x 16 of a wave's share, and what it gives is scaled and added
-// to the fp32 sums by vector instructions while the next ones run.
+// other, in steps of 128 bytes of the inner dimension; the steps of all its tiles form one
+// stream, as in ep_product_tile.hpp.  With block scales a step is a block: one matrix
+// instruction for each 16 x 16 of a wave's share, and what it gives is scaled and added to
+// the fp32 sums by vector instructions while the next ones run.  16-bit values take two,
+// which add to the sums themselves.
 //
-// Two stages of LDS (a step each).  A wave goes through its row tiles in order; before
-// the last two it has all fragments of the step in registers, waits for its own loads of
-// the next step, and meets the others: then the next step may be read and this one's
-// stage loaded over.  So a load has about a step to arrive, and fragments are read two
-// row tiles ahead, those of the weights behind their last use.
+// Two stages of LDS (a step each).  A wave goes through its row tiles in order; before the
+// last it has all fragments of the step in registers, waits for its own loads of the next
+// step, and meets the others: then the next step may be read and this one's stage loaded
+// over.  So there is one barrier a step, a load has nearly a step to arrive, and fragments
+// are read two row tiles ahead, those of the weights behind their last use.
+// Against steps of 64 bytes with four stages (ep_product_tile.hpp) the loads ask for whole
+// lines of 128 bytes, half as many requests, and barriers are half as many: 16-bit,
+// 65536 x 4096 x 4096 gated 1.77 to 1.70 ms (1297 TFLOP/s), 4096^3 115 to 107 us.
+// What bounds it: matrix instructions run 70 to 80% of the time at 1.5 GHz, which is what
+// the clock falls to; E4M3 50% at 1.8 GHz, where the scaling takes a third of the issue slots.
 //
 // LDS image: 128 bytes a row, chunk ^ (row & 7).  Columns of a wave's channel tiles, rows
-// past the group's and channels past the last as in ep_product_tile.hpp.  Behind the rows
-// a stage holds their scales of the block, and the two of the weights: of the tile's two
-// blocks of columns, or of its gates and its ups.
-template <int BM, int BN, int WM, int WN>
-struct Fp8Shape {
+// past the group's and channels past the last as in ep_product_tile.hpp.  With block scales
+// a stage holds behind the rows their scales of the block, and the two of the weights: of
+// the tile's two blocks of columns, or of its gates and its ups.
+template <int BM, int BN, int WM, int WN, bool BLOCKS>
+struct Tile128Shape {
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   static constexpr int CW = BN / WN;
   static constexpr int kRowBytes = 128;
   static constexpr int kScaleAt = (BM + BN) * kRowBytes;
-  static constexpr int kStage = kScaleAt + kThreads * 4;
+  static constexpr int kStage = kScaleAt + (BLOCKS ? kThreads * 4 : 0);
   static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;  // direct loads a wave and step
-  static constexpr int kLoads = kLoadsA + kLoadsW + 1;                        // and one of scales
+  static constexpr int kLoads = kLoadsA + kLoadsW + (BLOCKS ? 1 : 0);         // the last of scales
   static_assert(BM / kWave < kWaves, "a wave is left for the weights' scales");
   static size_t lds(int groups) { return 2 * (size_t)kStage + ((size_t)groups + 1) * 4; }
 };
 
 template <typename AR, typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
-__global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, int n_tiles) {
-  typedef Fp8Shape<BM, BN, WM, WN> S;
+__global__ __launch_bounds__(WM* WN* kWave) void matmul_tile128_kernel(MatmulArgs a, int n_tiles) {
+  constexpr bool kBlocks = AR::kScales == kBlockScales;
+  typedef Tile128Shape<BM, BN, WM, WN, kBlocks> S;
   constexpr int MT = S::MT, NT = S::NT, CW = S::CW;
   constexpr int BC = GATED ? BN / 2 : BN;  // columns of out
   constexpr int NO = GATED ? NT / 2 : NT;  // column tiles of out a wave
@@ -77,10 +84,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
     rw = buffer_of(w + (int64_t)x.c0 * K, any ? (int64_t)x.cols * K : 0);
     if (GATED) ru = buffer_of(w + (int64_t)(x.c0 + a.width) * K, any ? (int64_t)x.cols * K : 0);
     // (rows and columns past the tile's have the scale of its last)
-    if (wave < BM / kWave) {
+    if (kBlocks && wave < BM / kWave) {
       p_scale = a.a_scale + (x.m0 + min(wave * kWave + lane, x.rows - 1)) * a.a_row_step;
       p_scale_step = a.a_block_step;
-    } else {
+    } else if (kBlocks) {
       const int col = GATED ? x.c0 : min(x.c0 + (lane & 1) * 128, a.width - 1);
       p_scale = block_scales(a, GATED, x.g, col, GATED && (lane & 1));
       p_scale_step = 1;
@@ -92,7 +99,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   auto load_one = [&](int i) {
     const uint32_t k0 = (uint32_t)p_step * 128;
     uint8_t* st = tile_lds + p_stage;
-    if (i == S::kLoads - 1) {
+    if (kBlocks && i == S::kLoads - 1) {
       __builtin_amdgcn_global_load_lds((global_byte*)p_scale, (lds_byte*)(st + S::kScaleAt + wave * kWave * 4), 4, 0, 0);
     } else if (i < S::kLoadsA) {
       const int row = (i * S::kWaves + wave) * 8;
@@ -111,7 +118,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   };
   auto advance = [&]() {
     ++p_step;
-    p_scale += p_scale_step;
+    if (kBlocks) p_scale += p_scale_step;
     p_stage ^= S::kStage;
   };
 
@@ -128,22 +135,21 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   auto read_a = [&](uint32_t stage, int slot_, int m) {
     const uint8_t* at = tile_lds + (stage + a_at) + row_of(m) * S::kRowBytes;
     av[slot_] = AR::make(*(const i32x4*)(at + frag0), *(const i32x4*)(at + frag1));
-    sa[slot_] = *(const float*)(tile_lds + stage + sa_lane + row_of(m) * 4);
+    if (kBlocks) sa[slot_] = *(const float*)(tile_lds + stage + sa_lane + row_of(m) * 4);
   };
-  auto read_w = [&](uint32_t stage, int n) {
-    const uint8_t* at = tile_lds + (stage + w_at) + n * 16 * S::kRowBytes;
-    wv[n] = AR::make(*(const i32x4*)(at + frag0), *(const i32x4*)(at + frag1));
+  auto w_half = [&](uint32_t stage, int n, uint32_t frag) {
+    return *(const i32x4*)(tile_lds + (stage + w_at) + n * 16 * S::kRowBytes + frag);
   };
+  auto read_w = [&](uint32_t stage, int n) { wv[n] = AR::make(w_half(stage, n, frag0), w_half(stage, n, frag1)); };
   auto read_sw = [&](uint32_t stage) {
     const float* s = (const float*)(tile_lds + stage + S::kScaleAt) + BM;
     sw[0] = s[GATED ? 0 : wn * 16 * NO / 128];
     sw[1] = s[GATED ? 1 : wn * 16 * NO / 128];
   };
-  auto add = [&](int m) {  // the products in p, of row tile m, to the sums
+  // the products in p, of row tile m and column tile n, to the sums
+  auto add = [&](int m, int n) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = __builtin_fmaf(p[n][i], s_prev[n / NO], acc[m][n][i]);
+    for (int i = 0; i < 4; ++i) acc[m][n][i] = __builtin_fmaf(p[n][i], s_prev[n / NO], acc[m][n][i]);
   };
   // One step of MTN row tiles.
   auto step = [&](auto mtn) {
@@ -152,33 +158,53 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
     if (p_step == steps) next_tile();  // (here, since a branch further down lets the sums' additions sink past it)
 #pragma unroll
     for (int u = 0; u < MTN; ++u) {
-      if (u == MTN - 2) {
+      constexpr int kLast = MTN - 1;
+      if (u == kLast) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read_a(next, 0, 0);
+#pragma unroll
+        for (int i = 0; i < S::kLoads; i += 2) load_one(i);
       }
-      const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
+      if constexpr (kBlocks) {
+        const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int before = u == 0 ? MTN - 1 : u - 1;
+        for (int n = 0; n < NT; ++n) {
+          add(u == 0 ? kLast : u - 1, n);
+          p[n] = AR::mfma128(wv[n], av[u % 2]);
+          if (u == kLast) read_w(next, n);
+        }
+        s_prev[0] = s0;
+        s_prev[1] = s1;
+        if (u == kLast) read_sw(next);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[before][n][i] = __builtin_fmaf(p[n][i], s_prev[n / NO], acc[before][n][i]);
-        p[n] = AR::mfma128(wv[n], av[u % 2]);
-        if (u == MTN - 1) read_w(next, n);
+        for (int n = 0; n < NT; ++n) {
+          acc[u][n] = AR::mfma(wv[n].v[0], av[u % 2].v[0], acc[u][n]);
+          if (u == kLast) wv[n].v[0] = w_half(next, n, frag0);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[u][n] = AR::mfma(wv[n].v[1], av[u % 2].v[1], acc[u][n]);
+          if (u == kLast) wv[n].v[1] = w_half(next, n, frag1);
+        }
       }
-      s_prev[0] = s0;
-      s_prev[1] = s1;
-      if (u == MTN - 1) read_sw(next);
-      if (u + 2 < MTN)
-        read_a(cur, u % 2, u + 2);
-      else
-        read_a(next, u % 2, u + 2 - MTN);
-      if (u >= MTN - 2) {
+      if (u + 2 < MTN) read_a(cur, u % 2, u + 2);
+      if (u == kLast) {
+        read_a(next, 1, 1);
 #pragma unroll
-        for (int i = u - (MTN - 2); i < S::kLoads; i += 2) load_one(i);
+        for (int i = 1; i < S::kLoads; i += 2) load_one(i);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     advance();
     cur = next;
+  };
+  auto run = [&](auto mtn) {
+    for (int s = 0; s < steps; ++s) step(mtn);
+    if constexpr (kBlocks) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) add(decltype(mtn)::value - 1, n);
+    }
   };
 
   // the first two steps of the stream, and the first fragments
@@ -190,7 +216,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kLoads) : "memory");
 #pragma unroll
   for (int n = 0; n < NT; ++n) read_w(0, n);
-  read_sw(0);
+  if (kBlocks) read_sw(0);
   read_a(0, 0, 0);
   read_a(0, 1, 1);
 
@@ -200,17 +226,15 @@ __global__ __launch_bounds__(WM* WN* kWave) void fp8_tile_kernel(MatmulArgs a, i
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (kBlocks) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) p[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    s_prev[0] = s_prev[1] = 0.0f;
-    if (!HALVES || x.rows > BM / 2) {
-      for (int s = 0; s < steps; ++s) step(std::integral_constant<int, MT>{});
-      add(MT - 1);
-    } else {
-      constexpr int kHalf = HALVES ? MT / 2 : MT;
-      for (int s = 0; s < steps; ++s) step(std::integral_constant<int, kHalf>{});
-      add(kHalf - 1);
+      for (int n = 0; n < NT; ++n) p[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      s_prev[0] = s_prev[1] = 0.0f;
     }
+    if (!HALVES || x.rows > BM / 2)
+      run(std::integral_constant<int, MT>{});
+    else
+      run(std::integral_constant<int, HALVES ? MT / 2 : MT>{});
 
     int er = r, eq = q;
     asm volatile("" : "+v"(er), "+v"(eq));  // what follows is not kept in registers over the steps
