@@ -875,13 +875,13 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, fp8: bool = False, kee
     y = total = codes = scales = None
     if out is None:
         if keep:
-            y = torch.empty_strided((N, H), (H, 1), dtype=x.dtype, device=device)
+            y = torch.empty_like(x) if stride == H else torch.empty((N, H), dtype=x.dtype, device=device)
         if fp8:
             nb = _blocks(H)
             codes = torch.empty_strided((N, H), (H, 1), dtype=torch.uint8, device=device)
             scales = torch.empty_strided((N, nb), (nb, 1), dtype=torch.float32, device=device)
         if residual is not None:
-            total = torch.empty_strided((N, H), (H, 1), dtype=x.dtype, device=device)
+            total = torch.empty_like(x) if stride == H else torch.empty((N, H), dtype=x.dtype, device=device)
     else:
         if not (isinstance(out, tuple) and len(out) == 3):
             raise TypeError("out must be a tuple (y, quantized, total)")

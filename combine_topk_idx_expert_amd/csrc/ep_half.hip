@@ -82,7 +82,7 @@ int64_t slice_bytes(const GradPlan& p, int64_t rows, int width) {
 
 template <typename AR, typename IO, bool WEIGHTS, int BM, bool HALVES>
 ep_status launch_half_grad(const MatmulArgs& a, const GradPlan& p, hipStream_t s) {
-  typedef Tile128Shape<BM, 256, 2, 4, false> S;
+  typedef StepShape<BM, 256, 2, 4, false> S;
   const int64_t most = p.most * a.slices;
   if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "gradient of %lld tiles is too large", (long long)most);
   const int grid = (int)std::min<int64_t>(most, kCUs);

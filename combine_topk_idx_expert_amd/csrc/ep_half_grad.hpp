@@ -2,7 +2,7 @@
 // weights, in tiles staged through LDS; the gate's gradient.
 #pragma once
 
-#include "ep_product_tile128.hpp"
+#include "ep_product_tile.hpp"
 
 namespace ep {
 
@@ -15,7 +15,7 @@ namespace ep {
 // a lane's operand of the matrix instruction.
 //
 // Stream of steps, two stages, one barrier a step, order of tiles and halves as in
-// ep_product_tile128.hpp, with one difference: a wave's column tiles are 16 neighbouring
+// ep_product_tile.hpp, with one difference: a wave's column tiles are 16 neighbouring
 // columns each, and v_permlane16_swap gives a lane eight neighbours of a row at the end.
 // (65536 rows of 32 experts, 4096 x 4096: rows XXR ms, weights XXW, RATE.)
 //
@@ -102,7 +102,7 @@ __device__ __forceinline__ Tile locate_weights(const MatmulArgs& a, int m_tiles,
 
 template <typename AR, typename IO, bool WEIGHTS, int BM, int BN, int WM, int WN, bool HALVES>
 __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, int n_tiles) {
-  typedef Tile128Shape<BM, BN, WM, WN, false> S;
+  typedef StepShape<BM, BN, WM, WN, false> S;
   constexpr int MT = S::MT, NT = S::NT;
   constexpr int kImageA = BM * S::kRowBytes;
   static_assert(MT % 4 == 0 && NT == 4 && BN == 256 && (BM == 256 || BM == 128), "fragment registers and images");

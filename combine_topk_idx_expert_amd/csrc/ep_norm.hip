@@ -43,7 +43,8 @@ ep_status launch_norm(const NormArgs& a, hipStream_t s) {
 
 // Lanes of a row: 16, 32 or 64 (no barrier) where they hold it in one piece each, 64 with two
 // pieces where there are rows for all CUs; else four waves, and sixteen for the longest.
-// (32768 rows of 4096 bf16: four waves of two pieces 201 us, a wave of eight 475.)
+// (32768 rows of 4096 bf16: four waves of two pieces 201 us, a wave of eight 475.)  Rows for
+// less than all CUs take sixteen waves of one piece, for the latency.
 template <typename IO>
 ep_status launch_norm(const NormArgs& a, hipStream_t s) {
   constexpr int V = 16 / sizeof(typename IO::type);
@@ -52,6 +53,7 @@ ep_status launch_norm(const NormArgs& a, hipStream_t s) {
   if (pieces <= 32) return launch_norm<IO, 32, 1>(a, s);
   if (pieces <= 64) return launch_norm<IO, 64, 1>(a, s);
   if (pieces <= 2 * 64 && a.N >= 4 * kCUs) return launch_norm<IO, 64, 2>(a, s);
+  if (a.N <= kCUs && pieces > 256 && pieces <= 1024) return launch_norm<IO, 1024, 1>(a, s);
   if (pieces <= 128) return launch_norm<IO, 128, 1>(a, s);
   if (pieces <= 256) return launch_norm<IO, 256, 1>(a, s);
   if (pieces <= 2 * 256) return launch_norm<IO, 256, 2>(a, s);

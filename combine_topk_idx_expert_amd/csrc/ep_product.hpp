@@ -394,4 +394,80 @@ __global__ __launch_bounds__(KW* kWave) void matmul_split_kernel(MatmulArgs a) {
   }
 }
 
+// ---- tiles
+
+// Starts of the groups' row tiles: pre[g] tiles come before group g, pre[G] in
+// all.  Groups do not overlap, so there are at most M / BM + G tiles; ranges that
+// say otherwise are cut there, which keeps every index in range.
+template <int THREADS, int BM>
+__device__ void tile_starts(const MatmulArgs& a, int* pre) {
+  const int most = (int)(a.M / BM) + a.G;
+  for (int g = threadIdx.x; g < a.G; g += THREADS) {
+    int64_t lo, hi;
+    group_rows(a, g, lo, hi);
+    pre[g] = (int)((hi - lo + BM - 1) / BM);  // below 2^24
+  }
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    int carry = 0;
+    for (int g0 = 0; g0 < a.G; g0 += kWave) {
+      const int g = g0 + (int)threadIdx.x;
+      const int v = g < a.G ? pre[g] : 0;
+      int x = v;
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int y = __shfl_up(x, o, 64);
+        if ((int)threadIdx.x >= o) x += y;
+      }
+      if (g < a.G) pre[g] = min(carry + x - v, most);
+      carry = min(carry + __shfl(x, kWave - 1, 64), most);
+    }
+    if (threadIdx.x == 0) pre[a.G] = carry;
+  }
+  __syncthreads();
+}
+
+struct Tile {
+  int g;        // group
+  int64_t m0;   // first row
+  int rows;     // 1..BM
+  int c0;       // first column of out
+  int cols;     // 1..BN (BN / 2 gated)
+};
+
+// Tile t of all: the group is the last one whose tiles start at or before t
+// (64 starts are compared at once, of G <= 4096 in two rounds).  Within a group
+// strips of eight channel tiles, in each all row tiles, so that the tiles that
+// run at once on an XCD share both operands.
+template <int BM, int BC>
+__device__ __forceinline__ Tile locate(const MatmulArgs& a, const int* pre, int n_tiles, int t) {
+  Tile x;
+  int g = 0;
+  if (a.G > 1) {
+    const int lane = lane_id();
+    int base = 0, stride = (a.G + kWave - 1) / kWave;
+    if (stride > 1) {
+      const int i = lane * stride;
+      base = (__popcll(ballot(i < a.G && pre[min(i, a.G)] * n_tiles <= t)) - 1) * stride;
+    }
+    // stride <= 64 groups are left
+    const int i = base + lane;
+    g = base + __popcll(ballot((stride == 1 || lane < stride) && i < a.G && pre[min(i, a.G)] * n_tiles <= t)) - 1;
+    g = uniform(g);
+  }
+  const int first = uniform(pre[g]);
+  const int m_tiles = uniform(pre[g + 1]) - first;
+  const int in = t - first * n_tiles;
+  const int strip = in / (8 * m_tiles);
+  const int wide = min(8, n_tiles - strip * 8);
+  const int rest = in - strip * 8 * m_tiles;
+  int64_t lo, hi;
+  group_rows(a, g, lo, hi);
+  x.g = g;
+  x.m0 = lo + (int64_t)(rest / wide) * BM;
+  x.rows = (int)min((int64_t)BM, hi - x.m0);
+  x.c0 = (strip * 8 + rest % wide) * BC;
+  x.cols = min(BC, a.width - x.c0);
+  return x;
+}
+
 }  // namespace ep

@@ -4,9 +4,9 @@
 #include <algorithm>
 
 #include "ep_host.hpp"
+#include "ep_int8_tile.hpp"
 #include "ep_product.hpp"
 #include "ep_product_tile.hpp"
-#include "ep_product_tile128.hpp"
 
 namespace ep {
 
@@ -22,25 +22,21 @@ inline ep_status validate_matmul(int64_t num_rows, int32_t num_groups, int32_t o
   return EP_OK;
 }
 
-template <typename AR, typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
+template <typename AR, typename IO, bool GATED, int BM, bool HALVES>
 ep_status launch_matmul_tile(const MatmulArgs& a, hipStream_t s) {
-  typedef TileShape<BM, BN, WM, WN> S;
-  const int bc = GATED ? BN / 2 : BN;
+  const int bc = GATED ? 128 : 256;
   const int64_t n_tiles = (a.width + bc - 1) / bc;
   const int64_t most = (a.M / BM + a.G) * n_tiles;  // each group's last row tile may be partly filled
   if (most >= (int64_t)1 << 31) return fail(EP_ERR_OVERFLOW, "product of %lld tiles is too large", (long long)most);
   const int grid = (int)std::min<int64_t>(most, kCUs);
-#ifndef T128
-#define T128 (BM == 256 || AR::kScales == kBlockScales)
-#endif
-  if constexpr (AR::kScales != kRowScales && T128) {
-    typedef Tile128Shape<BM, BN, WM, WN, AR::kScales == kBlockScales> T;
-    matmul_tile128_kernel<AR, IO, GATED, BM, BN, WM, WN, HALVES><<<grid, T::kThreads, T::lds(a.G), s>>>(a, (int)n_tiles);
-    EP_LAUNCHED("matmul_tile128_kernel");
-  } else {
-    const size_t lds = S::lds(a.G, AR::kScales == kRowScales);
-    matmul_tile_kernel<AR, IO, GATED, BM, BN, WM, WN, HALVES><<<grid, S::kThreads, lds, s>>>(a, (int)n_tiles);
+  if constexpr (AR::kScales == kRowScales) {
+    typedef TileShape<BM, 256, 2, 4> S;
+    matmul_tile_kernel<IO, GATED, BM, 256, 2, 4, HALVES><<<grid, S::kThreads, S::lds(a.G), s>>>(a, (int)n_tiles);
     EP_LAUNCHED("matmul_tile_kernel");
+  } else {
+    typedef StepShape<BM, 256, 2, 4, AR::kScales == kBlockScales> S;
+    product_tile_kernel<AR, IO, GATED, BM, 256, 2, 4, HALVES><<<grid, S::kThreads, S::lds(a.G), s>>>(a, (int)n_tiles);
+    EP_LAUNCHED("product_tile_kernel");
   }
   return EP_OK;
 }
@@ -139,9 +135,20 @@ inline uint32_t matmul_kernels(int64_t M, int G, int width, bool gated) {
          (mean < 4 * kFewRows ? EP_KERNEL_SPLIT : 0);
 }
 
+// E4M3 and 16-bit dense products in tiles: the height whose rounds over the CUs cost less.  A
+// step of 256 rows takes 1.7 (E4M3 1.9) times one of 128 (22240 x 2112 x 326 gated, 174 or 348
+// tiles: 52 us by 256 rows, 59 by 128; 1003 x 2048 x 7168, 112 or 224: 36 by 128).
+inline bool tall_tiles(int64_t M, int64_t n_tiles) {
+  const int64_t tall = ((M + 255) / 256 * n_tiles + kCUs - 1) / kCUs, flat = ((M + 127) / 128 * n_tiles + kCUs - 1) / kCUs;
+  return 17 * tall <= 10 * flat;
+}
+
 template <typename AR, typename IO, bool GATED>
 ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
-  const uint32_t kernels = matmul_kernels(a.M, a.row_start ? a.G : 0, a.width, GATED);
+  uint32_t kernels = matmul_kernels(a.M, a.row_start ? a.G : 0, a.width, GATED);
+  if (AR::kScales != kRowScales && !a.row_start && kernels != EP_KERNEL_SPLIT)
+    kernels = tall_tiles(a.M, (a.width + (GATED ? 127 : 255)) / (GATED ? 128 : 256)) ? EP_KERNEL_TILES_256
+                                                                                     : EP_KERNEL_TILES_128;
   a.least = 0;
   a.most = a.M;
   if (kernels & EP_KERNEL_SPLIT) {
@@ -153,8 +160,8 @@ ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
   }
   // (bf16 fragments of E4M3 codes have no registers left for 256 rows)
   if constexpr (!std::is_same_v<AR, Fp8ExactMath>)
-    if (kernels & EP_KERNEL_TILES_256) return launch_matmul_tile<AR, IO, GATED, 256, 256, 2, 4, true>(a, s);
-  return launch_matmul_tile<AR, IO, GATED, 128, 256, 2, 4, false>(a, s);
+    if (kernels & EP_KERNEL_TILES_256) return launch_matmul_tile<AR, IO, GATED, 256, true>(a, s);
+  return launch_matmul_tile<AR, IO, GATED, 128, false>(a, s);
 }
 
 }  // namespace ep

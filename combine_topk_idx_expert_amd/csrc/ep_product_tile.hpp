@@ -1,4 +1,5 @@
-// ep_product_tile.hpp -- products of int8 and of 16-bit rows in tiles staged through LDS.
+// ep_product_tile.hpp -- products of E4M3 rows with block scales and of 16-bit rows in
+// tiles staged through LDS, in steps of 128 bytes.
 #pragma once
 
 #include <type_traits>
@@ -7,159 +8,54 @@
 
 namespace ep {
 
-// A workgroup of WM x WN waves computes tiles of BM rows x BN channels, one
-// after the other, in steps of 64 bytes of the inner dimension.  Both operands
-// have the inner dimension contiguous; their pieces go from memory straight to
-// LDS (16 bytes a lane) into a ring of four stages.
+// A workgroup of WM x WN waves computes tiles of BM rows x BN channels, one after the
+// other, in steps of 128 bytes of the inner dimension; the steps of all its tiles form one
+// stream, as in ep_int8_tile.hpp.  With block scales a step is a block: one matrix
+// instruction for each 16 x 16 of a wave's share, and what it gives is scaled and added to
+// the fp32 sums by vector instructions while the next ones run.  16-bit values take two,
+// which add to the sums themselves.
 //
-// The steps of all tiles of a workgroup form one stream.  In step s the waves
-//   - wait until their loads for step s + 1 have landed, and meet,
-//   - start the loads of step s + 3 (into the stage that step s - 1 left),
-//   - multiply step s, reading the fragments of its later row tiles and, near
-//     its end, the first ones of step s + 1.
-// So a load has two steps to arrive, no fragment is waited for behind a
-// barrier, and the next tile's first steps arrive during a tile's epilogue.
+// Two stages of LDS (a step each).  A wave goes through its row tiles in order; before the
+// last it has all fragments of the step in registers, waits for its own loads of the next
+// step, and meets the others: then the next step may be read and this one's stage loaded
+// over.  So there is one barrier a step, a load has nearly a step to arrive, and fragments
+// are read two row tiles ahead, those of the weights behind their last use.
+// Against steps of 64 bytes with four stages (ep_int8_tile.hpp) the loads ask for whole
+// lines of 128 bytes, half as many requests, and barriers are half as many: 16-bit,
+// 65536 x 4096 x 4096 gated 1.77 to 1.70 ms (1297 TFLOP/s), 4096^3 115 to 107 us.
+// What bounds it: matrix instructions run 70 to 80% of the time at 1.5 GHz, which is what
+// the clock falls to; E4M3 50% at 1.8 GHz, where the scaling takes a third of the issue slots.
 //
-// What bounds it for int8: a step takes 1470 cycles (256 x 256; 990 at 128 x 256) against 1024
-// (512) of products.  The direct loads alone come at ~24 bytes a clock and CU (a
-// probe of them from the L2: 42 to 54), and more stages change nothing; and
-// under int8 products the clock falls to 1.7-1.9 GHz of 2.4.  65536 rows of 64 groups,
-// 7168 x 4096 gated: 1775 us, 2.17e15 operations a second; 16384 rows, 2048 x 7168:
-// 341 us; 1003 x 2048 x 7168 (128 x 256): 22 us.
-//
-// LDS image of a stage: 64 bytes a row, its four 16-byte chunks in the order
-// chunk ^ order(row / 4 % 4), so that the lanes that ds_read_b128 serves
-// together (16 rows of one chunk, or 8 rows each of two) meet all banks; the
-// order (row / 4) % 4 itself had a conflict on every second read.  Direct loads
-// write lane l at l * 16, so the order is made by the addresses they read.
-//
-// Rows beyond the group's last one and channels beyond the last are beyond the
-// buffer descriptor's size and arrive as zeros; so do chunks of A past the
-// inner size (those of W may hold anything for int8, where their partners are zero).
-//
-// Row tiles of a wave: mt = 0..MT-1, in two halves of the tile, so that a tile
-// with at most BM / 2 rows costs half the products (HALVES).
-// GATED: of the 16 * NT channels of a wave the first half are gates and the
-// second half the ups of the same columns.
-//
-// Lane l of an MFMA gets channels (l / 16) * 4 + 0..3 of its first operand, so
-// the NO column tiles of a wave take their channels in turn, four at a time:
-// row i of column tile n is column (i / 4) * 4 * NO + n * 4 + i % 4, and a lane
-// ends with 4 * NO neighbouring columns of a row (16-byte stores, whole lines a
-// wave).
-template <int BM, int BN, int WM, int WN>
-struct TileShape {
+// LDS image: 128 bytes a row, chunk ^ (row & 7).  Columns of a wave's channel tiles, rows
+// past the group's and channels past the last as in ep_int8_tile.hpp.  With block scales
+// a stage holds behind the rows their scales of the block, and the two of the weights: of
+// the tile's two blocks of columns, or of its gates and its ups.
+template <int BM, int BN, int WM, int WN, bool BLOCKS>
+struct StepShape {
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
-  static constexpr int CW = BN / WN;  // channels of a wave
-  static constexpr int kStep = 64;
-  static constexpr int kStage = (BM + BN) * kStep;
-  static constexpr int kStages = 4;
-  static constexpr int kLoadsA = BM / 16 / kWaves, kLoadsW = BN / 16 / kWaves;  // direct loads a wave and step
-  static constexpr int kLoads = kLoadsA + kLoadsW;
-  static constexpr int kScales = BM + BN;  // floats of a tile
-  static_assert(kLoadsA >= 1 && kLoadsW >= 1, "a load covers 16 rows");
-  static size_t lds(int groups, bool scaled) {
-    return kStages * ((size_t)kStage + (scaled ? kScales * 4 : 0)) + ((size_t)groups + 1) * 4;
-  }
+  static constexpr int CW = BN / WN;
+  static constexpr int kRowBytes = 128;
+  static constexpr int kScaleAt = (BM + BN) * kRowBytes;
+  static constexpr int kStage = kScaleAt + (BLOCKS ? kThreads * 4 : 0);
+  static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;  // direct loads a wave and step
+  static constexpr int kLoads = kLoadsA + kLoadsW + (BLOCKS ? 1 : 0);         // the last of scales
+  static_assert(BM / kWave < kWaves, "a wave is left for the weights' scales");
+  static size_t lds(int groups) { return 2 * (size_t)kStage + ((size_t)groups + 1) * 4; }
 };
-
-__device__ __forceinline__ int chunk_order(int g) { return ((g ^ (g >> 1)) & 1) * 2 + (g >> 1); }  // 0, 2, 3, 1
-
-// All but the newest N of this wave's loads have landed, and every wave is here.
-template <int N>
-__device__ __forceinline__ void step_sync() {
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// Starts of the groups' row tiles: pre[g] tiles come before group g, pre[G] in
-// all.  Groups do not overlap, so there are at most M / BM + G tiles; ranges that
-// say otherwise are cut there, which keeps every index in range.
-template <int THREADS, int BM>
-__device__ void tile_starts(const MatmulArgs& a, int* pre) {
-  const int most = (int)(a.M / BM) + a.G;
-  for (int g = threadIdx.x; g < a.G; g += THREADS) {
-    int64_t lo, hi;
-    group_rows(a, g, lo, hi);
-    pre[g] = (int)((hi - lo + BM - 1) / BM);  // below 2^24
-  }
-  __syncthreads();
-  if (threadIdx.x < kWave) {
-    int carry = 0;
-    for (int g0 = 0; g0 < a.G; g0 += kWave) {
-      const int g = g0 + (int)threadIdx.x;
-      const int v = g < a.G ? pre[g] : 0;
-      int x = v;
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int y = __shfl_up(x, o, 64);
-        if ((int)threadIdx.x >= o) x += y;
-      }
-      if (g < a.G) pre[g] = min(carry + x - v, most);
-      carry = min(carry + __shfl(x, kWave - 1, 64), most);
-    }
-    if (threadIdx.x == 0) pre[a.G] = carry;
-  }
-  __syncthreads();
-}
-
-struct Tile {
-  int g;        // group
-  int64_t m0;   // first row
-  int rows;     // 1..BM
-  int c0;       // first column of out
-  int cols;     // 1..BN (BN / 2 gated)
-};
-
-// Tile t of all: the group is the last one whose tiles start at or before t
-// (64 starts are compared at once, of G <= 4096 in two rounds).  Within a group
-// strips of eight channel tiles, in each all row tiles, so that the tiles that
-// run at once on an XCD share both operands.
-template <int BM, int BC>
-__device__ __forceinline__ Tile locate(const MatmulArgs& a, const int* pre, int n_tiles, int t) {
-  Tile x;
-  int g = 0;
-  if (a.G > 1) {
-    const int lane = lane_id();
-    int base = 0, stride = (a.G + kWave - 1) / kWave;
-    if (stride > 1) {
-      const int i = lane * stride;
-      base = (__popcll(ballot(i < a.G && pre[min(i, a.G)] * n_tiles <= t)) - 1) * stride;
-    }
-    // stride <= 64 groups are left
-    const int i = base + lane;
-    g = base + __popcll(ballot((stride == 1 || lane < stride) && i < a.G && pre[min(i, a.G)] * n_tiles <= t)) - 1;
-    g = uniform(g);
-  }
-  const int first = uniform(pre[g]);
-  const int m_tiles = uniform(pre[g + 1]) - first;
-  const int in = t - first * n_tiles;
-  const int strip = in / (8 * m_tiles);
-  const int wide = min(8, n_tiles - strip * 8);
-  const int rest = in - strip * 8 * m_tiles;
-  int64_t lo, hi;
-  group_rows(a, g, lo, hi);
-  x.g = g;
-  x.m0 = lo + (int64_t)(rest / wide) * BM;
-  x.rows = (int)min((int64_t)BM, hi - x.m0);
-  x.c0 = (strip * 8 + rest % wide) * BC;
-  x.cols = min(BC, a.width - x.c0);
-  return x;
-}
 
 template <typename AR, typename IO, bool GATED, int BM, int BN, int WM, int WN, bool HALVES>
-__global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a, int n_tiles) {
-  typedef TileShape<BM, BN, WM, WN> S;
+__global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs a, int n_tiles) {
+  constexpr bool kBlocks = AR::kScales == kBlockScales;
+  typedef StepShape<BM, BN, WM, WN, kBlocks> S;
   constexpr int MT = S::MT, NT = S::NT, CW = S::CW;
   constexpr int BC = GATED ? BN / 2 : BN;  // columns of out
   constexpr int NO = GATED ? NT / 2 : NT;  // column tiles of out a wave
-  constexpr int kPair = 2 * S::kStage;     // the stages of an even and the next odd step
-  static_assert(MT % 4 == 0 && NT == 4, "fragment rings");
+  static_assert(MT % 4 == 0, "fragment registers take turns, also in half tiles");
+  static_assert(BC <= 256 && 128 % (16 * NO) == 0, "a wave's columns lie in one block");
   extern __shared__ uint8_t tile_lds[];
-  constexpr bool kScaled = AR::kScales == kRowScales;
-  typedef typename AR::acc acc_t;
-  float* const scales = (float*)(tile_lds + S::kStages * S::kStage);  // [kStages][BM + BN]
-  int* const pre = (int*)(scales + (kScaled ? S::kStages * S::kScales : 0));
+  int* const pre = (int*)(tile_lds + 2 * S::kStage);
   const int lane = lane_id();
   const int wave = uniform((int)threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
@@ -168,161 +64,192 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
   tile_starts<S::kThreads, BM>(a, pre);
   const int total = uniform(pre[a.G]) * n_tiles;
   const int K = a.K;
-  const int steps = (K + 2 * S::kStep - 1) / (2 * S::kStep) * 2;  // even: stages and registers take turns
-  // neighbouring tiles on one XCD (workgroups go round the 8 XCDs in turn)
+  const int steps = (K + 127) / 128;
   const int per = gridDim.x / 8;
   const int slot = gridDim.x % 8 == 0 ? ((int)blockIdx.x % 8) * per + (int)blockIdx.x / 8 : (int)blockIdx.x;
   if (slot >= total) return;
 
   // ---- producer: the stream of loads
-  const uint32_t chunk = (uint32_t)((lane & 3) ^ chunk_order(lane >> 4)) * 16;
-  const uint32_t lane_off = (uint32_t)(lane >> 2) * K + chunk;
-  const uint32_t lane_off_w = (uint32_t)((lane >> 4) * 4 * NO + ((lane >> 2) & 3)) * K + chunk;
-  int p_tile = slot, p_step = steps, p_ring = 0, p_stage = 0;
+  const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+  const uint32_t lane_off = (uint32_t)(lane >> 3) * K + chunk;
+  const uint32_t lane_off_w = (uint32_t)((lane >> 5) * 4 * NO + ((lane >> 3) & 3)) * K + chunk;
+  int p_tile = slot, p_step = steps;
+  uint32_t p_stage = 0;
   __amdgpu_buffer_rsrc_t ra, rw, ru;
-  auto next_tile = [&]() {  // descriptors of tile p_tile, and its scales on their way
+  const float* p_scale = a.a_scale;  // this lane's scale of the stream's next step
+  int64_t p_scale_step = 0;
+  auto next_tile = [&]() {
     const bool any = p_tile < total;
     const Tile x = locate<BM, BC>(a, pre, n_tiles, any ? p_tile : slot);
     const uint8_t* w = a.w + (int64_t)x.g * a.N * K;
     ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
     rw = buffer_of(w + (int64_t)x.c0 * K, any ? (int64_t)x.cols * K : 0);
     if (GATED) ru = buffer_of(w + (int64_t)(x.c0 + a.width) * K, any ? (int64_t)x.cols * K : 0);
-    const __amdgpu_buffer_rsrc_t rs = buffer_of(a.a_scale + x.m0, any ? x.rows * 4 : 0);
-    const __amdgpu_buffer_rsrc_t rc = buffer_of(a.w_scale + (int64_t)x.g * a.N, any ? a.N * 4 : 0);
-    float* dst = scales + p_ring * S::kScales;
-    for (int i = wave; kScaled && i < S::kScales / kWave; i += S::kWaves) {
-      int e = i * kWave + lane;
-      asm volatile("" : "+v"(e));
-      if (i * kWave < BM) {
-        load4_to_lds(rs, dst + i * kWave, (uint32_t)e * 4);
-      } else {
-        const int c = e - BM;  // gated: the columns' gates, then their ups
-        const int col = c % BC;
-        const int ch = x.c0 + col + (c >= BC ? a.width : 0);
-        load4_to_lds(rc, dst + i * kWave, col < x.cols ? (uint32_t)ch * 4 : kBeyond);
-      }
+    // (rows and columns past the tile's have the scale of its last)
+    if (kBlocks && wave < BM / kWave) {
+      p_scale = a.a_scale + (x.m0 + min(wave * kWave + lane, x.rows - 1)) * a.a_row_step;
+      p_scale_step = a.a_block_step;
+    } else if (kBlocks) {
+      const int col = GATED ? x.c0 : min(x.c0 + (lane & 1) * 128, a.width - 1);
+      p_scale = block_scales(a, GATED, x.g, col, GATED && (lane & 1));
+      p_scale_step = 1;
     }
-    p_ring = (p_ring + 1) % S::kStages;
     p_tile += gridDim.x;
     p_step = 0;
   };
   // load i of this wave's kLoads for the next step of the stream
   auto load_one = [&](int i) {
-    const uint32_t k0 = (uint32_t)p_step * S::kStep;
-    uint32_t off = lane_off + k0;
-    asm("" : "+v"(off));  // one register and an addition a load, rather than a register a load
-    uint8_t* st = tile_lds + p_stage * S::kStage;
-    if (i < S::kLoadsA) {
-      const int row = (i * S::kWaves + wave) * 16;
-      load16_to_lds(ra, st + row * S::kStep, k0 + chunk < (uint32_t)K ? off + (uint32_t)row * K : kBeyond);
+    const uint32_t k0 = (uint32_t)p_step * 128;
+    uint8_t* st = tile_lds + p_stage;
+    if (kBlocks && i == S::kLoads - 1) {
+      __builtin_amdgcn_global_load_lds((global_byte*)p_scale, (lds_byte*)(st + S::kScaleAt + wave * kWave * 4), 4, 0, 0);
+    } else if (i < S::kLoadsA) {
+      const int row = (i * S::kWaves + wave) * 8;
+      uint32_t off = lane_off + k0;
+      asm("" : "+v"(off));  // one register and an addition a load, rather than a register a load
+      load16_to_lds(ra, st + row * S::kRowBytes, k0 + chunk < (uint32_t)K ? off + (uint32_t)row * K : kBeyond);
     } else {
-      // LDS row `row` + 0..15: column tile n of wave column v
-      const int row = ((i - S::kLoadsA) * S::kWaves + wave) * 16;
-      const int v = row / CW, n = row % CW / 16;
-      uint32_t offw = lane_off_w + k0;
-      asm("" : "+v"(offw));
-      offw += (uint32_t)(v * 16 * NO + n % NO * 4) * K;
-      // (what follows a channel may be NaN; times zero only whole numbers vanish)
-      if (!kScaled && k0 + chunk >= (uint32_t)K) offw = kBeyond;
-      load16_to_lds(GATED && n >= NO ? ru : rw, st + (BM + row) * S::kStep, offw);
+      // LDS rows `row` + 0..7: half of column tile n of wave column v
+      const int row = ((i - S::kLoadsA) * S::kWaves + wave) * 8;
+      const int v = row / CW, n = row % CW / 16, half = row % 16 / 8;
+      uint32_t off = lane_off_w + k0;
+      asm("" : "+v"(off));
+      off += (uint32_t)(v * 16 * NO + n % NO * 4 + half * 8 * NO) * K;
+      load16_to_lds(GATED && n >= NO ? ru : rw, st + (BM + row) * S::kRowBytes, k0 + chunk < (uint32_t)K ? off : kBeyond);
     }
   };
   auto advance = [&]() {
     ++p_step;
-    p_stage = (p_stage + 1) % S::kStages;
+    if (kBlocks) p_scale += p_scale_step;
+    p_stage ^= S::kStage;
   };
 
   // ---- consumer
-  const int frag = r * S::kStep + ((q ^ chunk_order(r >> 2)) * 16);
-  const uint32_t a_lane = wm * (MT / 2) * 16 * S::kStep + frag;
-  const uint32_t w_lane = BM * S::kStep + wn * CW * S::kStep + frag;
-  uint32_t pair = 0;  // 0 or kPair: the current pair of stages
-  acc_t acc[MT][NT];
-  i32x4 av[4], wv[2][NT];
-  auto read_a = [&](uint32_t at, int h, int m) {
-    return *(const i32x4*)(tile_lds + at + h * S::kStage + (m < MT / 2 ? m : m - MT / 2 + BM / 32) * 16 * S::kStep);
+  // the two halves of a step in an image row
+  const uint32_t frag0 = r * S::kRowBytes + (q ^ (r & 7)) * 16, frag1 = frag0 ^ 64;
+  const uint32_t a_at = wm * (MT / 2) * 16 * S::kRowBytes, w_at = (BM + wn * CW) * S::kRowBytes;
+  const uint32_t sa_lane = S::kScaleAt + (wm * (MT / 2) * 16 + r) * 4;
+  uint32_t cur = 0;  // the current stage
+  f32x4 acc[MT][NT], p[NT];
+  typename AR::frag av[2], wv[NT];
+  float sa[2], sw[2], s_prev[2];
+  auto row_of = [](int m) { return m < MT / 2 ? m * 16 : (m - MT / 2) * 16 + BM / 2; };
+  auto read_a = [&](uint32_t stage, int slot_, int m) {
+    const uint8_t* at = tile_lds + (stage + a_at) + row_of(m) * S::kRowBytes;
+    av[slot_] = AR::make(*(const i32x4*)(at + frag0), *(const i32x4*)(at + frag1));
+    if (kBlocks) sa[slot_] = *(const float*)(tile_lds + stage + sa_lane + row_of(m) * 4);
   };
-  auto read_w = [&](uint32_t at, int h, int n) {
-    return *(const i32x4*)(tile_lds + at + h * S::kStage + n * 16 * S::kStep);
+  auto w_half = [&](uint32_t stage, int n, uint32_t frag) {
+    return *(const i32x4*)(tile_lds + (stage + w_at) + n * 16 * S::kRowBytes + frag);
   };
-  // One step; h: its place in the pair.
-  auto step = [&](auto hc, auto mtn) {
-    constexpr int h = decltype(hc)::value, MTN = decltype(mtn)::value;
-    step_sync<S::kLoads>();
-    if (p_step == steps) next_tile();
-    const uint32_t next = h ? kPair - pair : pair;
-    const uint32_t a_at = a_lane + pair, a_next = a_lane + next, w_next = w_lane + next;
+  auto read_w = [&](uint32_t stage, int n) { wv[n] = AR::make(w_half(stage, n, frag0), w_half(stage, n, frag1)); };
+  auto read_sw = [&](uint32_t stage) {
+    const float* s = (const float*)(tile_lds + stage + S::kScaleAt) + BM;
+    sw[0] = s[GATED ? 0 : wn * 16 * NO / 128];
+    sw[1] = s[GATED ? 1 : wn * 16 * NO / 128];
+  };
+  // the products in p, of row tile m and column tile n, to the sums
+  auto add = [&](int m, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[m][n][i] = __builtin_fmaf(p[n][i], s_prev[n / NO], acc[m][n][i]);
+  };
+  // One step of MTN row tiles.
+  auto step = [&](auto mtn) {
+    constexpr int MTN = decltype(mtn)::value;
+    const uint32_t next = cur ^ S::kStage;
+    if (p_step == steps) next_tile();  // (here, since a branch further down lets the sums' additions sink past it)
 #pragma unroll
     for (int u = 0; u < MTN; ++u) {
-      constexpr int kW0 = MTN > 4 ? 2 : 0;  // the next step's channel fragments: units kW0..kW0 + NT - 1
-      av[(u + 3) % 4] = u + 3 < MTN ? read_a(a_at, h, u + 3) : read_a(a_next, 1 - h, u + 3 - MTN);
-      if (u >= kW0 && u < kW0 + NT) wv[1 - h][u - kW0] = read_w(w_next, 1 - h, u - kW0);
+      constexpr int kLast = MTN - 1;
+      if (u == kLast) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read_a(next, 0, 0);
 #pragma unroll
-      for (int i = u; i < S::kLoads; i += MTN) load_one(i);
+        for (int i = 0; i < S::kLoads; i += 2) load_one(i);
+      }
+      if constexpr (kBlocks) {
+        const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        acc[u][n] = AR::mfma(wv[h][n], av[u % 4], acc[u][n]);
+        for (int n = 0; n < NT; ++n) {
+          add(u == 0 ? kLast : u - 1, n);
+          p[n] = AR::mfma128(wv[n], av[u % 2]);
+          if (u == kLast) read_w(next, n);
+        }
+        s_prev[0] = s0;
+        s_prev[1] = s1;
+        if (u == kLast) read_sw(next);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[u][n] = AR::mfma(wv[n].v[0], av[u % 2].v[0], acc[u][n]);
+          if (u == kLast) wv[n].v[0] = w_half(next, n, frag0);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[u][n] = AR::mfma(wv[n].v[1], av[u % 2].v[1], acc[u][n]);
+          if (u == kLast) wv[n].v[1] = w_half(next, n, frag1);
+        }
+      }
+      if (u + 2 < MTN) read_a(cur, u % 2, u + 2);
+      if (u == kLast) {
+        read_a(next, 1, 1);
+#pragma unroll
+        for (int i = 1; i < S::kLoads; i += 2) load_one(i);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     advance();
+    cur = next;
+  };
+  auto run = [&](auto mtn) {
+    for (int s = 0; s < steps; ++s) step(mtn);
+    if constexpr (kBlocks) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) add(decltype(mtn)::value - 1, n);
+    }
   };
 
-  // the first three steps of the stream, and the first fragments
-  for (int s = 0; s < 3; ++s) {
+  // the first two steps of the stream, and the first fragments
+  for (int s = 0; s < 2; ++s) {
     if (p_step == steps) next_tile();
     for (int i = 0; i < S::kLoads; ++i) load_one(i);
     advance();
   }
-  step_sync<2 * S::kLoads>();
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kLoads) : "memory");
 #pragma unroll
-  for (int n = 0; n < NT; ++n) wv[0][n] = read_w(w_lane, 0, n);
-#pragma unroll
-  for (int u = 0; u < 3; ++u) av[u] = read_a(a_lane, 0, u);
+  for (int n = 0; n < NT; ++n) read_w(0, n);
+  if (kBlocks) read_sw(0);
+  read_a(0, 0, 0);
+  read_a(0, 1, 1);
 
-  int c_ring = 0;
   for (int t = slot; t < total; t += gridDim.x) {
     const Tile x = locate<BM, BC>(a, pre, n_tiles, t);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = acc_t{0, 0, 0, 0};
-    auto run = [&](auto mtn) {
-      for (int s = 0; s < steps; s += 2) {
-        step(std::integral_constant<int, 0>{}, mtn);
-        step(std::integral_constant<int, 1>{}, mtn);
-        pair = kPair - pair;
-      }
-    };
+      for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (kBlocks) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) p[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      s_prev[0] = s_prev[1] = 0.0f;
+    }
     if (!HALVES || x.rows > BM / 2)
       run(std::integral_constant<int, MT>{});
     else
       run(std::integral_constant<int, HALVES ? MT / 2 : MT>{});
 
-    // epilogue: a lane holds columns wn * 16 * NO + q * 4 * NO + 0..4 * NO - 1 of
-    // row r of every row tile
-    const float* sa = scales + c_ring * S::kScales;
-    c_ring = (c_ring + 1) % S::kStages;
     int er = r, eq = q;
     asm volatile("" : "+v"(er), "+v"(eq));  // what follows is not kept in registers over the steps
     const int col = wn * 16 * NO + eq * 4 * NO;
-    float sw[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sw[n][i] = !kScaled ? 1.0f : sa[BM + (n < NO ? 0 : BC) + col + (n % NO) * 4 + i];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int row = (m < MT / 2 ? 0 : BM / 2) + wm * (MT / 2) * 16 + (m % (MT / 2)) * 16 + er;
+      const int row = wm * (MT / 2) * 16 + row_of(m) + er;
       if (row >= x.rows) continue;
-      const float s = kScaled ? sa[row] : 1.0f;
       float y[NT * 4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[n * 4 + i] = (float)acc[m][n][i];
-          if (kScaled) y[n * 4 + i] = y[n * 4 + i] * s * sw[n][i];
-        }
+        for (int i = 0; i < 4; ++i) y[n * 4 + i] = acc[m][n][i];
       store_row<IO, GATED, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
     }
   }
