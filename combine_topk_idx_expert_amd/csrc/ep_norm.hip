@@ -69,8 +69,10 @@ struct NormTeams {
   int lanes, nc, groups;
 };
 
-// Every workgroup writes a row of fp32 sums, so there are no more than fill the card, and for
-// few rows one for every four.
+// Every workgroup writes a row of fp32 sums, so there are no more than the card can use, and
+// for few rows one for every four.  (262144 x 4096 bf16: 256 lanes of two pieces, three
+// workgroups a CU 1610 us, four without the next row ahead 1690; 512 lanes of one 1840.
+// 65536 x 2048: three 177 us, five 201.)
 NormTeams norm_teams(int32_t type, int64_t N, int32_t H) {
   const int v = 16 / (int)type_bytes(type);
   const int pieces = (H + v - 1) / v;
@@ -80,9 +82,9 @@ NormTeams norm_teams(int32_t type, int64_t N, int32_t H) {
   else if (pieces <= 64) t.lanes = 64;
   else if (pieces <= 128) t.lanes = 128;
   else if (pieces <= 256) t.lanes = 256;
-  else if (pieces <= 512) t.lanes = 512;
+  else if (pieces <= 512) t.lanes = 256, t.nc = 2;
   else while (t.nc * 1024 < pieces) t.nc *= 2;
-  const int64_t full = kCUs * (t.lanes == 1024 ? 1 : t.lanes == 512 ? 2 : t.lanes == 128 ? 10 : 5);
+  const int64_t full = kCUs * (t.lanes == 1024 ? 1 : t.lanes == 256 ? 3 : t.lanes == 128 ? 10 : 5);
   const int64_t rows = t.lanes <= kWave ? 256 / t.lanes : 1;  // at once in a workgroup
   const int64_t all = (N + rows - 1) / rows;
   t.groups = (int)std::min(full, std::max<int64_t>(std::min<int64_t>(all, kCUs), all / 4));
@@ -102,8 +104,8 @@ ep_status launch_norm_backward(const NormBwdArgs& a, const NormTeams& t, hipStre
   if (t.lanes == 32) return launch_norm_backward<IO, 32, 1>(a, s);
   if (t.lanes == 64) return launch_norm_backward<IO, 64, 1>(a, s);
   if (t.lanes == 128) return launch_norm_backward<IO, 128, 1>(a, s);
+  if (t.lanes == 256 && t.nc == 2) return launch_norm_backward<IO, 256, 2>(a, s);
   if (t.lanes == 256) return launch_norm_backward<IO, 256, 1>(a, s);
-  if (t.lanes == 512) return launch_norm_backward<IO, 512, 1>(a, s);
   if (t.nc == 1) return launch_norm_backward<IO, 1024, 1>(a, s);
   if (t.nc == 2) return launch_norm_backward<IO, 1024, 2>(a, s);
   if (t.nc == 4) return launch_norm_backward<IO, 1024, 4>(a, s);

@@ -400,14 +400,14 @@ struct NormBwdArgs {
 // their room) and the weight's gradient of its columns over all its rows.  A workgroup's teams
 // join those at the end, and norm_weight_kernel those of all workgroups, in a fixed order.
 // The two sums over a row share one barrier, and rows in turn use one of two places for
-// them.  Where there is room the weight stays in registers and the next row is on its way
+// them.  Where registers allow the weight stays in registers and the next row is on its way
 // while a row is worked on.
 template <typename IO, int L, int NC>
 __global__ __launch_bounds__(L <= kWave ? 256 : L) void norm_backward_kernel(NormBwdArgs a) {
   constexpr int V = 16 / sizeof(typename IO::type);
   constexpr int W = L <= kWave ? 1 : L / kWave;
   constexpr int kTeams = L <= kWave ? 256 / L : 1;  // of a workgroup
-  constexpr bool kAhead = NC * V <= 8;
+  constexpr bool kAhead = NC * V <= (L == 256 ? 16 : 8);
   static_assert(kTeams == 1 || NC == 1, "a workgroup's teams join one piece a lane");
   __shared__ float part[2][2][W];
   __shared__ float redo[3][W];
