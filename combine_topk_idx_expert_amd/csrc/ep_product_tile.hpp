@@ -73,41 +73,48 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
   const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
   const uint32_t lane_off = (uint32_t)(lane >> 3) * K + chunk;
   const uint32_t lane_off_w = (uint32_t)((lane >> 5) * 4 * NO + ((lane >> 3) & 3)) * K + chunk;
-  int p_tile = slot, p_step = steps;
+  // Where the loads of a tile come from.  (The one behind the last tile reads zeros.)
+  struct Source {
+    __amdgpu_buffer_rsrc_t a, w, u;
+    const float* scale;  // this lane's, of the next step
+    int64_t scale_step;
+  };
+  int p_tile = slot, p_step = 0;
   uint32_t p_stage = 0;
-  __amdgpu_buffer_rsrc_t ra, rw, ru;
-  const float* p_scale = a.a_scale;  // this lane's scale of the stream's next step
-  int64_t p_scale_step = 0;
-  auto next_tile = [&]() {
+  auto next_source = [&]() {
     const bool any = p_tile < total;
     const Tile x = locate<BM, BC>(a, pre, n_tiles, any ? p_tile : slot);
     const uint8_t* w = a.w + (int64_t)x.g * a.N * K;
-    ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
-    rw = buffer_of(w + (int64_t)x.c0 * K, any ? (int64_t)x.cols * K : 0);
-    if (GATED) ru = buffer_of(w + (int64_t)(x.c0 + a.width) * K, any ? (int64_t)x.cols * K : 0);
+    Source n;
+    n.a = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
+    n.w = buffer_of(w + (int64_t)x.c0 * K, any ? (int64_t)x.cols * K : 0);
+    n.u = GATED ? buffer_of(w + (int64_t)(x.c0 + a.width) * K, any ? (int64_t)x.cols * K : 0) : n.w;
     // (rows and columns past the tile's have the scale of its last)
+    n.scale = nullptr;
+    n.scale_step = 0;
     if (kBlocks && wave < BM / kWave) {
-      p_scale = a.a_scale + (x.m0 + min(wave * kWave + lane, x.rows - 1)) * a.a_row_step;
-      p_scale_step = a.a_block_step;
+      n.scale = a.a_scale + (x.m0 + min(wave * kWave + lane, x.rows - 1)) * a.a_row_step;
+      n.scale_step = a.a_block_step;
     } else if (kBlocks) {
       const int col = GATED ? x.c0 : min(x.c0 + (lane & 1) * 128, a.width - 1);
-      p_scale = block_scales(a, GATED, x.g, col, GATED && (lane & 1));
-      p_scale_step = 1;
+      n.scale = block_scales(a, GATED, x.g, col, GATED && (lane & 1));
+      n.scale_step = 1;
     }
     p_tile += gridDim.x;
-    p_step = 0;
+    return n;
   };
+  Source src = next_source(), next_src = src;
   // load i of this wave's kLoads for the next step of the stream
   auto load_one = [&](int i) {
     const uint32_t k0 = (uint32_t)p_step * 128;
     uint8_t* st = tile_lds + p_stage;
     if (kBlocks && i == S::kLoads - 1) {
-      __builtin_amdgcn_global_load_lds((global_byte*)p_scale, (lds_byte*)(st + S::kScaleAt + wave * kWave * 4), 4, 0, 0);
+      __builtin_amdgcn_global_load_lds((global_byte*)src.scale, (lds_byte*)(st + S::kScaleAt + wave * kWave * 4), 4, 0, 0);
     } else if (i < S::kLoadsA) {
       const int row = (i * S::kWaves + wave) * 8;
       uint32_t off = lane_off + k0;
       asm("" : "+v"(off));  // one register and an addition a load, rather than a register a load
-      load16_to_lds(ra, st + row * S::kRowBytes, k0 + chunk < (uint32_t)K ? off + (uint32_t)row * K : kBeyond);
+      load16_to_lds(src.a, st + row * S::kRowBytes, k0 + chunk < (uint32_t)K ? off + (uint32_t)row * K : kBeyond);
     } else {
       // LDS rows `row` + 0..7: half of column tile n of wave column v
       const int row = ((i - S::kLoadsA) * S::kWaves + wave) * 8;
@@ -115,14 +122,24 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
       uint32_t off = lane_off_w + k0;
       asm("" : "+v"(off));
       off += (uint32_t)(v * 16 * NO + n % NO * 4 + half * 8 * NO) * K;
-      load16_to_lds(GATED && n >= NO ? ru : rw, st + (BM + row) * S::kRowBytes, k0 + chunk < (uint32_t)K ? off : kBeyond);
+      load16_to_lds(GATED && n >= NO ? src.u : src.w, st + (BM + row) * S::kRowBytes, k0 + chunk < (uint32_t)K ? off : kBeyond);
     }
   };
+  // The stream goes on by a step, in next_src after a tile's last.
   auto advance = [&]() {
-    ++p_step;
-    if (kBlocks) p_scale += p_scale_step;
+    const bool last = p_step == steps - 1;
+    src.a = last ? next_src.a : src.a;
+    src.w = last ? next_src.w : src.w;
+    if (GATED) src.u = last ? next_src.u : src.u;
+    if (kBlocks) {
+      src.scale = last ? next_src.scale : src.scale + src.scale_step;
+      src.scale_step = last ? next_src.scale_step : src.scale_step;
+    }
+    p_step = last ? 0 : p_step + 1;
     p_stage ^= S::kStage;
   };
+
+  constexpr int kFirst = 2;  // loads right behind the barrier
 
   // ---- consumer
   // the two halves of a step in an image row
@@ -156,8 +173,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
   // One step of MTN row tiles.
   auto step = [&](auto mtn) {
     constexpr int MTN = decltype(mtn)::value;
+    constexpr int kLoading = MTN > 2 ? MTN / 2 - 1 : 1;  // row tiles that share the loads
+    constexpr int kEach = (S::kLoads - kFirst + kLoading - 1) / kLoading;
     const uint32_t next = cur ^ S::kStage;
-    if (p_step == steps) next_tile();  // (here, since a branch further down lets the sums' additions sink past it)
+    // (here, since a branch further down lets the sums' additions sink past it)
+    if (p_step == steps - 1) next_src = next_source();
 #pragma unroll
     for (int u = 0; u < MTN; ++u) {
       constexpr int kLast = MTN - 1;
@@ -165,8 +185,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         read_a(next, 0, 0);
 #pragma unroll
-        for (int i = 0; i < S::kLoads; i += 2) load_one(i);
+        for (int i = 0; i < kFirst; ++i) load_one(i);
       }
+      // the other loads of the step that the last row tile of the step before began
+#pragma unroll
+      for (int i = kFirst + u * kEach; i < min(kFirst + (u + 1) * kEach, S::kLoads); ++i) load_one(i);
+      if (u == kLoading - 1) advance();
       if constexpr (kBlocks) {
         const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
 #pragma unroll
@@ -193,12 +217,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
       if (u + 2 < MTN) read_a(cur, u % 2, u + 2);
       if (u == kLast) {
         read_a(next, 1, 1);
-#pragma unroll
-        for (int i = 1; i < S::kLoads; i += 2) load_one(i);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance();
     cur = next;
   };
   auto run = [&](auto mtn) {
@@ -209,13 +230,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
     }
   };
 
-  // the first two steps of the stream, and the first fragments
-  for (int s = 0; s < 2; ++s) {
-    if (p_step == steps) next_tile();
-    for (int i = 0; i < S::kLoads; ++i) load_one(i);
-    advance();
-  }
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kLoads) : "memory");
+  // the stream's first step and the beginning of its second, and the first fragments
+  for (int i = 0; i < S::kLoads; ++i) load_one(i);
+  if (steps == 1) next_src = next_source();
+  advance();
+  for (int i = 0; i < kFirst; ++i) load_one(i);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kFirst) : "memory");
 #pragma unroll
   for (int n = 0; n < NT; ++n) read_w(0, n);
   if (kBlocks) read_sw(0);
