@@ -44,6 +44,10 @@ struct Strided {
   }
 };
 
+__device__ __forceinline__ Strided pick(bool first, const Strided& x, const Strided& y) {
+  return Strided{first ? x.at : y.at, first ? x.left : y.left, first ? x.stride : y.stride, first ? x.tail : y.tail};
+}
+
 // Where lane's 16 bytes of a load of 1 KiB come from, from the step's first index on:
 // loads go round the waves, WIDTH values an index.
 template <int WIDTH>
@@ -152,38 +156,46 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
   const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
   const uint32_t lane_off_a = WEIGHTS ? strided_source<BM>(wave, lane, (uint32_t)K) : (uint32_t)(lane >> 3) * K + chunk;
   const uint32_t lane_off_w = strided_source<BN>(wave, lane, (uint32_t)a.width * 2);
-  int p_tile = slot, p_step = 0, p_steps = 0;
+  // Where the loads of a tile come from.  (The one behind the last tile reads zeros.)
+  struct Source {
+    int steps;
+    Strided a, w;                // strided operands (a: of the weights' gradient)
+    __amdgpu_buffer_rsrc_t rows; // rows' gradient: d's rows, and the bytes of them that the tile needs
+    uint32_t from, to;
+  };
+  int p_tile = slot, p_step = 0;
   uint32_t p_stage = 0;
-  __amdgpu_buffer_rsrc_t ra, rw;
-  Strided sa{}, sw{};
-  uint32_t a_from = 0, a_to = 0;  // rows' gradient: the bytes of d's rows that the tile needs
-  auto next_tile = [&]() {
+  auto next_source = [&]() {
     const bool any = p_tile < total;
     const int t = any ? p_tile : slot;
     const Tile x = tile(t);
     const int64_t row = (int64_t)a.width * 2;
     int64_t lo, hi;
     inner(t, x, lo, hi);
-    p_steps = steps_of(lo, hi);
+    Source s;
+    s.steps = steps_of(lo, hi);
+    s.from = (uint32_t)lo * 2;
+    s.to = (uint32_t)hi * 2;
     const int64_t n = any ? hi - lo : 0;
     if constexpr (WEIGHTS) {
-      sa.start(a.a + lo * K + x.m0 * 2, n, K, K - x.m0 * 2);
-      sw.start(a.w + lo * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
+      s.a.start(a.a + lo * K + x.m0 * 2, n, K, K - x.m0 * 2);
+      s.w.start(a.w + lo * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
+      s.rows = buffer_of(a.a, 0);
     } else {
-      ra = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
-      a_from = (uint32_t)lo * 2;
-      a_to = (uint32_t)hi * 2;
-      sw.start(a.w + ((int64_t)x.g * a.N + lo) * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
+      s.a.start(a.a, 0, 0, 0);
+      s.w.start(a.w + ((int64_t)x.g * a.N + lo) * row + (int64_t)x.c0 * 2, n, row, row - (int64_t)x.c0 * 2);
+      s.rows = buffer_of(a.a + x.m0 * K, any ? (int64_t)x.rows * K : 0);
     }
     p_tile += gridDim.x;
-    p_step = 0;
+    return s;
   };
-  // descriptors of the stream's next step
+  Source src = next_source(), next_src = src;
+  __amdgpu_buffer_rsrc_t ra, rw;  // of the stream's next step
   auto describe = [&]() {
-    if (p_step == p_steps) next_tile();
-    if constexpr (WEIGHTS) ra = sa.step();
-    rw = sw.step();
+    ra = WEIGHTS ? src.a.step() : src.rows;
+    rw = src.w.step();
   };
+  describe();
   // load i of this wave's kLoads for the next step of the stream
   auto load_one = [&](int i) {
     uint8_t* st = tile_lds + p_stage;
@@ -195,9 +207,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
         // 1 KiB is 512 / BM indexes
         load16_to_lds(ra, st + at, off + (uint32_t)(i * S::kWaves * (512 / BM)) * K);
       } else {
-        const uint32_t k0 = a_from + (uint32_t)p_step * S::kRowBytes;
+        const uint32_t k0 = src.from + (uint32_t)p_step * S::kRowBytes;
         off += k0 + (uint32_t)((i * S::kWaves + wave) * 8) * K;
-        load16_to_lds(ra, st + at, k0 + chunk < a_to ? off : kBeyond);
+        load16_to_lds(ra, st + at, k0 + chunk < src.to ? off : kBeyond);
       }
     } else {
       const int j = i - S::kLoadsA;
@@ -207,9 +219,21 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
                     off + (uint32_t)(j * S::kWaves * (512 / BN) * 2) * a.width);
     }
   };
+  // The stream goes on by a step, in next_src after a tile's last.
   auto advance = [&]() {
-    ++p_step;
+    const bool last = p_step == src.steps - 1;
+    if (WEIGHTS) {
+      src.a = pick(last, next_src.a, src.a);
+    } else {
+      src.rows = last ? next_src.rows : src.rows;
+      src.from = last ? next_src.from : src.from;
+      src.to = last ? next_src.to : src.to;
+    }
+    src.w = pick(last, next_src.w, src.w);
+    src.steps = last ? next_src.steps : src.steps;
+    p_step = last ? 0 : p_step + 1;
     p_stage ^= S::kStage;
+    describe();
   };
 
   // ---- consumer
@@ -239,8 +263,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
   // One step of MTN row tiles.
   auto step = [&](auto mtn) {
     constexpr int MTN = decltype(mtn)::value;
+    constexpr int kLoading = MTN * 5 / 8;  // row tiles that share the loads
+    constexpr int kEach = (S::kLoads - S::kFirst + kLoading - 1) / kLoading;
     const uint32_t next = cur ^ S::kStage;
-    describe();
+    if (p_step == src.steps - 1) next_src = next_source();
 #pragma unroll
     for (int u = 0; u < MTN; ++u) {
       constexpr int kLast = MTN - 1;
@@ -248,8 +274,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         read_a(next, 0, 0);
 #pragma unroll
-        for (int i = 0; i < S::kLoads; i += 2) load_one(i);
+        for (int i = 0; i < S::kFirst; ++i) load_one(i);
       }
+      // the other loads of the step that the last row tile of the step before began
+#pragma unroll
+      for (int i = S::kFirst + u * kEach; i < min(S::kFirst + (u + 1) * kEach, S::kLoads); ++i) load_one(i);
+      if (u == kLoading - 1) advance();
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -258,24 +288,18 @@ __global__ __launch_bounds__(WM* WN* kWave) void half_grad_kernel(MatmulArgs a, 
           if (u == kLast) wv[n].v[h] = w_half(next, n, h);
         }
       if (u + 2 < MTN) read_a(cur, u % 2, u + 2);
-      if (u == kLast) {
-        read_a(next, 1, 1);
-#pragma unroll
-        for (int i = 1; i < S::kLoads; i += 2) load_one(i);
-      }
+      if (u == kLast) read_a(next, 1, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance();
     cur = next;
   };
 
-  // the first two steps of the stream, and the first fragments
-  for (int s = 0; s < 2; ++s) {
-    describe();
-    for (int i = 0; i < S::kLoads; ++i) load_one(i);
-    advance();
-  }
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kLoads) : "memory");
+  // the stream's first step and the beginning of its second, and the first fragments
+  for (int i = 0; i < S::kLoads; ++i) load_one(i);
+  if (src.steps == 1) next_src = next_source();
+  advance();
+  for (int i = 0; i < S::kFirst; ++i) load_one(i);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kFirst) : "memory");
 #pragma unroll
   for (int n = 0; n < NT; ++n) wv[n] = AR::make(w_half(0, n, 0), w_half(0, n, 1));
   read_a(0, 0, 0);

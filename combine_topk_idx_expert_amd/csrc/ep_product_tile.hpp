@@ -18,8 +18,10 @@ namespace ep {
 // Two stages of LDS (a step each).  A wave goes through its row tiles in order; before the
 // last it has all fragments of the step in registers, waits for its own loads of the next
 // step, and meets the others: then the next step may be read and this one's stage loaded
-// over.  So there is one barrier a step, a load has nearly a step to arrive, and fragments
-// are read two row tiles ahead, those of the weights behind their last use.
+// over, two loads at once and the others over the first row tiles of the next step (all at
+// once they hold up the products behind them: E4M3 7%, 16-bit 3%).  So there is one barrier
+// a step, a load has at least three row tiles to arrive, and fragments are read two row
+// tiles ahead, those of the weights behind their last use.
 // Against steps of 64 bytes with four stages (ep_int8_tile.hpp) the loads ask for whole
 // lines of 128 bytes, half as many requests, and barriers are half as many: 16-bit,
 // 65536 x 4096 x 4096 gated 1.77 to 1.70 ms (1297 TFLOP/s), 4096^3 115 to 107 us.
@@ -41,6 +43,7 @@ struct StepShape {
   static constexpr int kStage = kScaleAt + (BLOCKS ? kThreads * 4 : 0);
   static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;  // direct loads a wave and step
   static constexpr int kLoads = kLoadsA + kLoadsW + (BLOCKS ? 1 : 0);         // the last of scales
+  static constexpr int kFirst = 2;  // of them right behind the barrier
   static_assert(BM / kWave < kWaves, "a wave is left for the weights' scales");
   static size_t lds(int groups) { return 2 * (size_t)kStage + ((size_t)groups + 1) * 4; }
 };
@@ -139,9 +142,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
     p_stage ^= S::kStage;
   };
 
-  constexpr int kFirst = 2;  // loads right behind the barrier
-
-  // ---- consumer
+    // ---- consumer
   // the two halves of a step in an image row
   const uint32_t frag0 = r * S::kRowBytes + (q ^ (r & 7)) * 16, frag1 = frag0 ^ 64;
   const uint32_t a_at = wm * (MT / 2) * 16 * S::kRowBytes, w_at = (BM + wn * CW) * S::kRowBytes;
@@ -173,8 +174,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
   // One step of MTN row tiles.
   auto step = [&](auto mtn) {
     constexpr int MTN = decltype(mtn)::value;
-    constexpr int kLoading = MTN > 2 ? MTN / 2 - 1 : 1;  // row tiles that share the loads
-    constexpr int kEach = (S::kLoads - kFirst + kLoading - 1) / kLoading;
+    constexpr int kLoading = MTN * 5 / 8;  // row tiles that share the loads
+    constexpr int kEach = (S::kLoads - S::kFirst + kLoading - 1) / kLoading;
     const uint32_t next = cur ^ S::kStage;
     // (here, since a branch further down lets the sums' additions sink past it)
     if (p_step == steps - 1) next_src = next_source();
@@ -185,11 +186,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         read_a(next, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kFirst; ++i) load_one(i);
+        for (int i = 0; i < S::kFirst; ++i) load_one(i);
       }
       // the other loads of the step that the last row tile of the step before began
 #pragma unroll
-      for (int i = kFirst + u * kEach; i < min(kFirst + (u + 1) * kEach, S::kLoads); ++i) load_one(i);
+      for (int i = S::kFirst + u * kEach; i < min(S::kFirst + (u + 1) * kEach, S::kLoads); ++i) load_one(i);
       if (u == kLoading - 1) advance();
       if constexpr (kBlocks) {
         const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
@@ -234,8 +235,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
   for (int i = 0; i < S::kLoads; ++i) load_one(i);
   if (steps == 1) next_src = next_source();
   advance();
-  for (int i = 0; i < kFirst; ++i) load_one(i);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kFirst) : "memory");
+  for (int i = 0; i < S::kFirst; ++i) load_one(i);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kFirst) : "memory");
 #pragma unroll
   for (int n = 0; n < NT; ++n) read_w(0, n);
   if (kBlocks) read_sw(0);
