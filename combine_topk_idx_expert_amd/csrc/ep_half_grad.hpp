@@ -17,7 +17,7 @@ namespace ep {
 // Stream of steps, two stages, one barrier a step, order of tiles and halves as in
 // ep_product_tile.hpp, with one difference: a wave's column tiles are 16 neighbouring
 // columns each, and v_permlane16_swap gives a lane eight neighbours of a row at the end.
-// (65536 rows of 32 experts, 4096 x 4096: rows XXR ms, weights XXW, RATE.)
+// (65536 rows of 32 experts, 4096 x 4096: rows 1.9 ms, weights 2.0, 1.1e15 operations a second.)
 //
 // Image of a strided operand: index k has 512 (256) bytes, blocks of 32 bytes (16 values)
 // in the order block ^ f(k), f(k) = k % 4 + 4 (k / 8 % 2): the eight k whose blocks 32

@@ -23,10 +23,12 @@ namespace ep {
 // a step, a load has at least three row tiles to arrive, and fragments are read two row
 // tiles ahead, those of the weights behind their last use.
 // Against steps of 64 bytes with four stages (ep_int8_tile.hpp) the loads ask for whole
-// lines of 128 bytes, half as many requests, and barriers are half as many: 16-bit,
-// 65536 x 4096 x 4096 gated 1.77 to 1.70 ms (1297 TFLOP/s), 4096^3 115 to 107 us.
-// What bounds it: matrix instructions run 70 to 80% of the time at 1.5 GHz, which is what
-// the clock falls to; E4M3 50% at 1.8 GHz, where the scaling takes a third of the issue slots.
+// lines of 128 bytes, half as many requests, and barriers are half as many.  Measured:
+// 16-bit, 65536 x 4096 x 4096 gated 1.64 to 1.69 ms (64-byte steps 1.85), 4096^3 102 us (115),
+// 8192^3 815 to 945 us with the clock; E4M3, 65536 x 4096 x 4096 gated 1.01 to 1.05 ms.
+// What bounds it (8192^3): 16-bit matrix instructions run 66% of the cycles, the rest goes to
+// barriers and to reads of LDS waited for; E4M3's 52%, and vector instructions, two thirds of
+// them the scaling, 38%, which leaves a tenth.  Under either the clock falls to 1.5 to 1.9 GHz.
 //
 // LDS image: 128 bytes a row, chunk ^ (row & 7).  Columns of a wave's channel tiles, rows
 // past the group's and channels past the last as in ep_int8_tile.hpp.  With block scales
@@ -164,7 +166,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
   auto read_sw = [&](uint32_t stage) {
     const float* s = (const float*)(tile_lds + stage + S::kScaleAt) + BM;
     sw[0] = s[GATED ? 0 : wn * 16 * NO / 128];
-    sw[1] = s[GATED ? 1 : wn * 16 * NO / 128];
+    if (GATED) sw[1] = s[1];
   };
   // the products in p, of row tile m and column tile n, to the sums
   auto add = [&](int m, int n) {
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
       for (int i = S::kFirst + u * kEach; i < min(S::kFirst + (u + 1) * kEach, S::kLoads); ++i) load_one(i);
       if (u == kLoading - 1) advance();
       if constexpr (kBlocks) {
-        const float s0 = sa[u % 2] * sw[0], s1 = sa[u % 2] * sw[1];
+        const float s0 = sa[u % 2] * sw[0], s1 = GATED ? sa[u % 2] * sw[1] : s0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           add(u == 0 ? kLast : u - 1, n);
@@ -216,9 +218,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
         }
       }
       if (u + 2 < MTN) read_a(cur, u % 2, u + 2);
-      if (u == kLast) {
-        read_a(next, 1, 1);
-      }
+      if (u == kLast) read_a(next, 1, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
     cur = next;
