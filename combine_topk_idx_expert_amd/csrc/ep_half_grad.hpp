@@ -392,10 +392,12 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restri
     IO::unpack(__builtin_nontemporal_load((const typename IO::piece*)((const T*)grad + i * 8)), d);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      // (an infinite exponential gives s = 0, and g s its limit 0 for finite g)
+      // an infinite exponential gives s = 0, and g s its limit 0 for finite g: a gate that was
+      // rounded to an infinity counts as fp32's largest
+      if (__builtin_isinf(g[j])) g[j] = __builtin_copysignf(0x1.fffffep127f, g[j]);
       const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g[j]));
-      du[j] = d[j] * g[j] * s;
-      dg[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+      du[j] = d[j] * (g[j] * s);
+      dg[j] = d[j] * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
     }
     IO::store_piece((T*)out + at, dg);
     IO::store_piece((T*)out + at + width, du);

@@ -150,6 +150,24 @@ def test_gates_at_the_ends():
     assert_close(gw.t(), d, off, "d")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gates_that_were_rounded_to_infinities(dtype):
+    """Their gate is shut or open; NaN stays NaN."""
+    pre = torch.zeros(8, 16, device=DEV, dtype=dtype)
+    pre[:, 8:] = 3.0
+    pre[0, :8], pre[1, :8], pre[2, :8] = float("-inf"), float("inf"), float("nan")
+    grad = torch.full((8, 8), 2.0, device=DEV, dtype=dtype)
+    one = torch.zeros(1, 8, device=DEV, dtype=dtype)
+    one[0, 0] = 1.0
+    w = torch.zeros(16, 8, device=DEV, dtype=dtype)
+    # a row at a time, since an infinity times another row's zero is NaN: column 0 of grad_w is its gradient
+    for r, (dg, du) in enumerate([(0.0, 0.0), (6.0, float("inf")), (float("nan"), float("nan")), (3.0, 0.0)]):
+        _, g = ep.matmul_backward(one, w, grad[r:r + 1], gated=True, pre=pre[r:r + 1].contiguous(),
+                                  out=(None, torch.empty(16, 8, device=DEV)))
+        np.testing.assert_allclose(f64(g[:8, 0]), np.full(8, dg))
+        np.testing.assert_allclose(f64(g[8:, 0]), np.full(8, du))
+
+
 def test_gradients_agree_with_differences():
     """Forward and backward pass along random directions of the 64-bit function."""
     r = np.random.default_rng(1)
