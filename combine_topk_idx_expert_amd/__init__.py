@@ -13,6 +13,10 @@ call raises.
     y = experts(recv_x, ...)                                  # caller's work
     out = combine(h, y, topk_weights)
     h.free()
+
+Around it: the router (route, route_backward), the norm (rms_norm, rms_norm_backward), quantising
+(quantize_int8, quantize_fp8) and the experts' products (matmul_int8, matmul_fp8, matmul,
+matmul_backward).
 """
 
 from __future__ import annotations

@@ -213,7 +213,8 @@ def lib() -> ctypes.CDLL:
         L.ep_matmul.argtypes = [i32, vp, i64, vp, i32, vp, vp, i32, i32, u32, vp, vp, vp]
         L.ep_matmul_backward_workspace.argtypes = [i64, i32, i32, i32, u32, ctypes.POINTER(i64)]
         L.ep_matmul_backward.argtypes = [i32, vp, i64, vp, vp, vp, i32, vp, vp, i32, i32, u32, vp, vp, i32, vp, vp]
-        for fn in ("ep_matmul_fp8", "ep_matmul", "ep_matmul_backward_workspace", "ep_matmul_backward", "ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward"):
+        for fn in ("ep_quantize_fp8", "ep_rms_norm", "ep_rms_norm_backward_workspace", "ep_rms_norm_backward",
+                   "ep_matmul_fp8", "ep_matmul", "ep_matmul_backward_workspace", "ep_matmul_backward"):
             getattr(L, fn).restype = i32
         L.ep_debug_e4m3_encode.argtypes = [vp, vp, i64, vp]
         L.ep_debug_e4m3_encode.restype = i32
