@@ -1073,9 +1073,11 @@ def matmul_backward(a, w, grad, rows=None, gated: bool = False, pre=None, out=No
         if ga is not None:
             _require(ga, dtype, (M, K), "grad_a", device)
         if gw is not None:
-            if gw.dtype == torch.float32:
+            if isinstance(gw, torch.Tensor) and gw.dtype == torch.float32:
                 gcode = 0
             _require(gw, torch.float32 if gcode == 0 else dtype, w.shape, "grad_w", device)
+        if ga is None and gw is None:
+            raise ValueError("grad_a and grad_w are None: nothing would be written")
     flags = _GATED if gated else 0
     size = ctypes.c_int64()
     _check(lib().ep_matmul_backward_workspace(M, G, K, N, flags, ctypes.byref(size)))

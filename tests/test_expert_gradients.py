@@ -118,6 +118,32 @@ def test_group_gradients_match_plain(counts, K, N, gated):
             close_product(gw[e], d.T.copy(), f64(a[s:s + n]).T.copy(), off.T.copy(), dtype, ("grad_w", e))
 
 
+@pytest.mark.parametrize("M,K,N", [(30000, 1000, 64), (20000, 1024, 128), (9000, 1504, 192)])
+def test_rows_of_few_channels_over_many_tiles(M, K, N):
+    """One, two and three steps a tile of the rows' gradient, more tiles than workgroups."""
+    a, w, grad, _ = case(1, M, K, N, 0, False, torch.bfloat16)
+    ga, gw = ep.matmul_backward(a, w, grad, out=(torch.empty_like(a), torch.empty(N, K, device=DEV)))
+    d, off = product_gradient(f64(grad), None, torch.bfloat16)
+    close_product(ga, d, f64(w).T.copy(), off, torch.bfloat16, "grad_a")
+    close_product(gw, d.T.copy(), f64(a).T.copy(), off.T.copy(), torch.bfloat16, "grad_w")
+
+
+@pytest.mark.parametrize("counts,K,N", [([40, 64, 65, 128, 1, 0, 130, 200] * 4, 1024, 1024), ([1, 0, 2] * 1365, 24, 32)],
+                         ids=["many tiles", "many groups"])
+def test_weights_of_groups_of_few_rows(counts, K, N):
+    start, count, M = groups_of(counts)
+    G = len(counts)
+    a, w, grad, pre = case(2, M, K, N, G, True, torch.bfloat16)
+    ga, gw = ep.matmul_backward(a, w, grad, rows=as_rows(start, count), gated=True, pre=pre)
+    for e, (s, n) in enumerate(spans(start, count)):
+        if n == 0:
+            assert not gw[e].any()
+            continue
+        d, off = product_gradient(f64(grad[s:s + n]), f64(pre[s:s + n]), torch.bfloat16)
+        close_product(ga[s:s + n], d, f64(w[e]).T.copy(), off, torch.bfloat16, ("grad_a", e))
+        close_product(gw[e], d.T.copy(), f64(a[s:s + n]).T.copy(), off.T.copy(), torch.bfloat16, ("grad_w", e))
+
+
 @pytest.mark.parametrize("gated", [False, True])
 def test_one_gradient_without_the_other_and_no_rows(gated):
     for rows in (None, as_rows([0, 100], [90, 0])):
@@ -217,3 +243,32 @@ def test_gradients_on_streams_and_in_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_two_graphs_replayed_at_once():
+    """Workspaces (the gate's gradient, slices, the norm's partial sums) belong to a graph each."""
+    graphs = []
+    for k in range(2):
+        a, w, grad, pre = case(10 + k, 6000, 256, 512, 0, True, torch.bfloat16)
+        wn = torch.ones(256, device=DEV)
+
+        def step(a=a, w=w, grad=grad, pre=pre, wn=wn):
+            ga, gw = ep.matmul_backward(a, w, grad, gated=True, pre=pre)
+            return [ga, gw, *ep.rms_norm_backward(a, wn, ga)]
+
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out, want, torch.cuda.Stream(), step))  # (step holds the inputs that the graph reads)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, out, _, stream, _ in graphs:
+            with torch.cuda.stream(stream):
+                for t in out:
+                    t.zero_()
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _, _ in graphs:
+            assert all(torch.equal(x, y) for x, y in zip(out, want))

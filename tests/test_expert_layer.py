@@ -203,6 +203,8 @@ def test_refusals_before_any_launch():
                 lambda: ep.matmul(x, w[None], rows=as_rows([0, 1], [1, 1])),
                 lambda: ep.matmul_backward(x, w, randn(3, 8, 16), gated=True),
                 lambda: ep.matmul_backward(x, w, randn(3, 8, 31)),
+                lambda: ep.matmul_backward(x, w, randn(3, 8, 32), out=(None, None)),
+                lambda: ep.matmul_backward(x, w, randn(3, 8, 32), out=(None, torch.empty(33, 64, device=DEV))),
                 lambda: ep.quantize_fp8(x, out=(torch.empty(8, 64, dtype=torch.uint8, device=DEV),
                                                 torch.empty(1, 8, device=DEV)))):
         with pytest.raises(ValueError):
@@ -210,6 +212,8 @@ def test_refusals_before_any_launch():
     for bad in (lambda: ep.rms_norm(x, w[0].half()), lambda: ep.rms_norm(x, w[0], residual=x.float()),
                 lambda: ep.rms_norm(x.double(), w[0].double()), lambda: ep.matmul(x.float(), w.float()),
                 lambda: ep.matmul(x, w.half()), lambda: ep.matmul_fp8((x, x), (w, w)), lambda: ep.matmul_fp8(x, w),
+                lambda: ep.matmul_backward(x, w, randn(3, 8, 32), out=(None, w.half())),
+                lambda: ep.matmul_backward(x, w, randn(3, 8, 32), out=(None, 1.0)),
                 lambda: ep.rms_norm(x, w[0], out=[x, None, None]), lambda: ep.quantize_fp8([1.0])):
         with pytest.raises(TypeError):
             bad()

@@ -283,6 +283,37 @@ def test_half_nan_and_infinite_values_stay_in_their_row_and_channel(M, K, N):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("M,K,N", [(4100, 128, 3330), (4100, 256, 3330), (4100, 384, 3330)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_short_inner_sizes_over_many_tiles(M, K, N, gated):
+    """One, two and three steps a tile, more tiles than workgroups."""
+    check_fp8_dense(M, K, N, gated, torch.bfloat16, True)
+    a, w = half_case(1, M, K // 2, N, 0, torch.bfloat16)
+    ref, tol, _, _ = expected(f64(a), f64(w), gated, torch.bfloat16)
+    assert_close(ep.matmul(a, w, gated=gated), ref, tol, "product")
+
+
+@pytest.mark.parametrize("op", ["fp8", "half"])
+def test_as_many_groups_as_experts_may_be(op):
+    G, K, N = 4096, 32, 24
+    count = np.random.default_rng(1).integers(0, 4, G)
+    count[7], count[4000] = 300, 170
+    start, count, M = groups_of(count)
+    rows = as_rows(start, count)
+    if op == "fp8":
+        a, sa, w, sw = fp8_case(1, M, K, N, G, True, False)
+        got = ep.matmul_fp8((a, sa), (w, sw), rows=rows, gated=True, out_dtype=torch.float32)
+        x, v, dropped, t = fp8_values(a, sa, False), lambda e: fp8_weights(w[e], sw[e], True), 0.0, torch.float32
+    else:
+        a, w = half_case(1, M, K, N, G, torch.bfloat16)
+        got = ep.matmul(a, w, rows=rows, gated=True)
+        x, v, dropped, t = f64(a), lambda e: f64(w[e]), 0.0, torch.bfloat16
+    for e, (s, n) in enumerate(spans(start, count)):
+        if n:
+            ref, tol, _, _ = expected(x[s:s + n], v(e), True, t, dropped)
+            assert_close(got[s:s + n], ref, tol, ("group", e))
+
+
 @pytest.mark.parametrize("op", ["fp8", "half"])
 def test_ranges_outside_the_rows_are_cut(op):
     """Row ranges come from the device: those past the rows are cut, those that start outside are empty."""
