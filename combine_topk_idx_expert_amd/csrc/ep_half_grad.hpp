@@ -376,8 +376,10 @@ __global__ __launch_bounds__(256) void join_slices_kernel(MatmulArgs a, const fl
 
 // Gradient of the gate: with out = silu(g) u,
 //   dg = grad u s (1 + g (1 - s)),  du = grad g s,  s = 1 / (1 + exp(-g)).
-// Rounded to the rows' type, as the products' operands have to be; their sums are fp32.
-// Bound by memory.
+// Rounded to the rows' type, as the products' operands have to be; their sums are fp32.  s
+// comes from the hardware's exp2 and reciprocal: a step of fp32 each, and less than |g| 2^-23
+// of s from the rounded exponent (2^-16 at most, where s is not yet 0), far below that
+// rounding.  Bound by memory: 65536 x 2048 bf16 233 us, 5.8 TB/s.
 template <typename IO>
 __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restrict__ pre, const void* __restrict__ grad,
                                                             int64_t pieces, int width, void* __restrict__ out) {
