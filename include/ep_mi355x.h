@@ -538,7 +538,8 @@ ep_status ep_matmul(int32_t type, const void *a, int64_t num_rows, const void *w
 
 /* ep_matmul_backward -- gradients of ep_matmul.
  *   grad  device, [num_rows, outer] of `type` ([num_rows, outer / 2] gated): that of out.
- *   pre   gated: what ep_matmul kept; else NULL.
+ *   pre   gated: what ep_matmul kept; else NULL.  A projection that its rounding made
+ *         infinite counts as fp32's largest, so a shut gate's gradients are 0.
  *   grad_a       device, [num_rows, inner] of `type`, or NULL.  Rows of no group are
  *                left as they were.
  *   grad_w       device, [num_groups, outer, inner] ([outer, inner] if num_groups is
