@@ -764,8 +764,9 @@ ep_status ep_matmul_int8(const int8_t* a, const float* a_scale, int64_t num_rows
   if (misaligned(a, 16) || misaligned(w, 16) || misaligned(out, 16) || misaligned(a_scale, 4) ||
       misaligned(w_scale, 4) || misaligned(row_start, 8) || misaligned(row_count, 4))
     return fail(EP_ERR_SHAPE, "a / w / out must be 16-byte aligned, other arrays aligned to their element size");
-  MatmulArgs m{(const uint8_t*)a, a_scale, (const uint8_t*)w, w_scale, num_groups > 0 ? row_start : nullptr, num_groups > 0 ? row_count : nullptr,
-               out, num_rows, std::max(num_groups, 1), outer, inner, gated ? outer / 2 : outer, 0, num_rows, nullptr, 0, 0, 1};
+  MatmulArgs m{(const uint8_t*)a, a_scale, (const uint8_t*)w, w_scale, num_groups > 0 ? row_start : nullptr,
+               num_groups > 0 ? row_count : nullptr, out, num_rows, std::max(num_groups, 1), outer, inner,
+               gated ? outer / 2 : outer, 0, num_rows, nullptr, 0, 0, 1};
   return with_type(out_type, [&](auto io) {
     return gated ? launch_matmul<Int8Math, decltype(io), true>(m, (hipStream_t)stream)
                  : launch_matmul<Int8Math, decltype(io), false>(m, (hipStream_t)stream);

@@ -239,7 +239,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void matmul_tile_kernel(MatmulArgs a
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[n * 4 + i] = (float)acc[m][n][i] * s * sw[n][i];
-      store_row<IO, GATED, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
+      store_row<IO, GATED, false, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup

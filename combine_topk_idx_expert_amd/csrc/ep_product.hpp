@@ -192,12 +192,13 @@ __device__ __forceinline__ void store_cols(void* out, int64_t at, int col, int e
 
 // The scaled sums of NT channel tiles of one row (tile n: columns col + 4 n + 0..3 of
 // out; gated, the second half of the tiles are the ups of the first half's columns) to
-// out, and before the gate to pre where it is asked for.
-template <typename IO, bool GATED, int NT>
+// out, and before the gate to pre where it is asked for (PRE: 16-bit products may.  Asked in
+// the gated int8 tiles, too, it took 209 registers for 203 and 17 scalar spills more).
+template <typename IO, bool GATED, bool PRE, int NT>
 __device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int col, int end, const float* y) {
   constexpr int NO = GATED ? NT / 2 : NT;
   if constexpr (GATED) {
-    if (a.pre) {
+    if (PRE && a.pre) {
       const int64_t at = row * a.N + col;
       store_cols<IO, NO * 4>(a.pre, at, col, end, y);
       store_cols<IO, NO * 4>(a.pre, at + a.width, col, end, y + NO * 4);
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(KW* kWave) void matmul_split_kernel(MatmulArgs a) {
               y[n * 4 + i] = y[n * 4 + i] * s * ws[(n < NO ? 0 : a.width) + c];
             }
           }
-        store_row<IO, GATED, NT>(a, m0 + row, col, a.width, y);
+        store_row<IO, GATED, AR::kScales == kNoScales, NT>(a, m0 + row, col, a.width, y);
       }
     }
     __syncthreads();

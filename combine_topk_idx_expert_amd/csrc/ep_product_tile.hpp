@@ -144,7 +144,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
     p_stage ^= S::kStage;
   };
 
-    // ---- consumer
+  // ---- consumer
   // the two halves of a step in an image row
   const uint32_t frag0 = r * S::kRowBytes + (q ^ (r & 7)) * 16, frag1 = frag0 ^ 64;
   const uint32_t a_at = wm * (MT / 2) * 16 * S::kRowBytes, w_at = (BM + wn * CW) * S::kRowBytes;
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tile_kernel(MatmulArgs 
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[n * 4 + i] = acc[m][n][i];
-      store_row<IO, GATED, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
+      store_row<IO, GATED, !kBlocks, NT>(a, x.m0 + row, x.c0 + col, x.c0 + x.cols, y);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
