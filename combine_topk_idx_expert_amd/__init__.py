@@ -36,9 +36,11 @@ from ._native import (  # noqa: F401
     buffer_size_hint,
     combine,
     comm_stream,
+    debug_backward_plan,
     debug_copy,
     debug_e4m3_encode,
     debug_matmul_kernels,
+    debug_product_kernels,
     dispatch,
     dispatch_cached,
     expert_rows,

@@ -9,7 +9,7 @@ import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libep_mi355x.so"
-EP_ABI_VERSION = 7
+EP_ABI_VERSION = 8
 
 # dispatch flags
 _FP8 = 1
@@ -224,6 +224,10 @@ def lib() -> ctypes.CDLL:
         L.ep_debug_copy.restype = i32
         L.ep_debug_matmul_kernels.argtypes = [i64, i32, i32, u32, ctypes.POINTER(u32)]
         L.ep_debug_matmul_kernels.restype = i32
+        L.ep_debug_product_kernels.argtypes = [i64, i32, i32, u32, i32, ctypes.POINTER(u32)]
+        L.ep_debug_product_kernels.restype = i32
+        L.ep_debug_backward_plan.argtypes = [i64, i32, i32, i32, u32, ctypes.POINTER(i32)]
+        L.ep_debug_backward_plan.restype = i32
         L.ep_last_error.argtypes = []
         L.ep_last_error.restype = ctypes.c_char_p
         L.ep_abi_version.argtypes = []
@@ -1107,6 +1111,23 @@ def debug_matmul_kernels(num_rows: int, num_groups: int, outer: int, gated: bool
     bits = ctypes.c_uint32()
     _check(lib().ep_debug_matmul_kernels(num_rows, num_groups, outer, _GATED if gated else 0, ctypes.byref(bits)))
     return tuple(name for bit, name in _KERNELS.items() if bits.value & bit)
+
+
+def debug_product_kernels(num_rows: int, num_groups: int, outer: int, gated: bool = False, dtype=None) -> tuple:
+    """The same for matmul and matmul_fp8, by ep_debug_product_kernels; dtype: the result's (default
+    bfloat16; float32: matmul_fp8 alone).  Host only."""
+    bits = ctypes.c_uint32()
+    code = 1 if dtype is None else _type(dtype, "dtype")
+    _check(lib().ep_debug_product_kernels(num_rows, num_groups, outer, _GATED if gated else 0, code, ctypes.byref(bits)))
+    return tuple(name for bit, name in _KERNELS.items() if bits.value & bit)
+
+
+def debug_backward_plan(num_rows: int, num_groups: int, inner: int, outer: int, gated: bool = False) -> tuple:
+    """How matmul_backward cuts its gradients for these sizes, by ep_debug_backward_plan: ((rows of a
+    tile, slices) of the rows' gradient, the same of the weights').  Host only."""
+    plan = (ctypes.c_int32 * 4)()
+    _check(lib().ep_debug_backward_plan(num_rows, num_groups, inner, outer, _GATED if gated else 0, plan))
+    return (plan[0], plan[1]), (plan[2], plan[3])
 
 
 def debug_copy(dst, src):

@@ -30,3 +30,17 @@ extern "C" ep_status ep_matmul_fp8(const uint8_t* a, const float* a_scale, int64
                  : launch_matmul<AR, decltype(io), false>(m, (hipStream_t)stream);
   });
 }
+
+extern "C" ep_status ep_debug_product_kernels(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags,
+                                              int32_t out_type, uint32_t* kernels) {
+  if (!kernels) return fail(EP_ERR_NULL, "kernels is NULL");
+  const ep_status st = validate_matmul(num_rows, num_groups, outer, flags);
+  if (st != EP_OK) return st;
+  if (!known_type(out_type)) return fail(EP_ERR_SHAPE, "unknown element type %d", out_type);
+  const bool gated = flags & EP_MATMUL_GATED;
+  const int width = gated ? outer / 2 : outer;
+  *kernels = num_rows == 0             ? 0
+             : out_type == EP_TYPE_F32 ? product_kernels<Fp8ExactMath>(num_rows, num_groups, width, gated)
+                                       : product_kernels<Bf16Math>(num_rows, num_groups, width, gated);
+  return EP_OK;
+}

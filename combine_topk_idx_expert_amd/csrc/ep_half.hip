@@ -50,7 +50,8 @@ int best_slices(int64_t tiles, int64_t inner, int64_t result_bytes) {
 }
 
 // Rows' gradient: width = inner of the product, its inner dimension are the channels.  Tiles of
-// 256 rows where the product of that width takes them.
+// 256 rows where an int8 product of that width takes them (the rule that dense 16-bit products
+// have instead, tall_tiles, was not timed for gradients).
 GradPlan plan_rows(int64_t M, int G, int inner, int outer) {
   const bool tall = matmul_kernels(M, G, inner, false) & EP_KERNEL_TILES_256;
   const int rows = tall ? 256 : 128;
@@ -218,6 +219,19 @@ ep_status ep_matmul_backward(int32_t type, const void* a, int64_t num_rows, cons
   hipStream_t s = (hipStream_t)stream;
   return type == EP_TYPE_BF16 ? matmul_backward<Bf16Math, Bf16>(r, g, pre, grad, workspace, grad_w_type, s)
                               : matmul_backward<F16Math, F16>(r, g, pre, grad, workspace, grad_w_type, s);
+}
+
+ep_status ep_debug_backward_plan(int64_t num_rows, int32_t num_groups, int32_t inner, int32_t outer, uint32_t flags,
+                                 int32_t* plan) {
+  if (!plan) return fail(EP_ERR_NULL, "plan is NULL");
+  const ep_status st = validate_half_backward(EP_TYPE_BF16, num_rows, num_groups, inner, outer, flags);
+  if (st != EP_OK) return st;
+  const GradPlan r = plan_rows(num_rows, num_groups, inner, outer), w = plan_weights(num_rows, num_groups, inner, outer);
+  plan[0] = r.tall ? 256 : 128;
+  plan[1] = r.slices;
+  plan[2] = w.tall ? 256 : 128;
+  plan[3] = w.slices;
+  return EP_OK;
 }
 
 }  // extern "C"

@@ -143,12 +143,22 @@ inline bool tall_tiles(int64_t M, int64_t n_tiles) {
   return 17 * tall <= 10 * flat;
 }
 
+// EP_KERNEL_* of a product's launches: matmul_kernels, and for E4M3 and 16-bit rows the
+// height above.  (bf16 fragments of E4M3 codes have no registers left for 256 rows.)
+template <typename AR>
+uint32_t product_kernels(int64_t M, int G, int width, bool gated) {
+  uint32_t kernels = matmul_kernels(M, G, width, gated);
+  if (AR::kScales != kRowScales && G == 0 && kernels != EP_KERNEL_SPLIT)
+    kernels = tall_tiles(M, (width + (gated ? 127 : 255)) / (gated ? 128 : 256)) ? EP_KERNEL_TILES_256
+                                                                               : EP_KERNEL_TILES_128;
+  if (std::is_same_v<AR, Fp8ExactMath> && (kernels & EP_KERNEL_TILES_256))
+    kernels ^= EP_KERNEL_TILES_256 | EP_KERNEL_TILES_128;
+  return kernels;
+}
+
 template <typename AR, typename IO, bool GATED>
 ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
-  uint32_t kernels = matmul_kernels(a.M, a.row_start ? a.G : 0, a.width, GATED);
-  if (AR::kScales != kRowScales && !a.row_start && kernels != EP_KERNEL_SPLIT)
-    kernels = tall_tiles(a.M, (a.width + (GATED ? 127 : 255)) / (GATED ? 128 : 256)) ? EP_KERNEL_TILES_256
-                                                                                     : EP_KERNEL_TILES_128;
+  const uint32_t kernels = product_kernels<AR>(a.M, a.row_start ? a.G : 0, a.width, GATED);
   a.least = 0;
   a.most = a.M;
   if (kernels & EP_KERNEL_SPLIT) {
@@ -158,7 +168,6 @@ ep_status launch_matmul(MatmulArgs a, hipStream_t s) {
     if (st != EP_OK || kernels == EP_KERNEL_SPLIT) return st;
     a.least = kFewRows + 1;
   }
-  // (bf16 fragments of E4M3 codes have no registers left for 256 rows)
   if constexpr (!std::is_same_v<AR, Fp8ExactMath>)
     if (kernels & EP_KERNEL_TILES_256) return launch_matmul_tile<AR, IO, GATED, 256, true>(a, s);
   return launch_matmul_tile<AR, IO, GATED, 128, false>(a, s);

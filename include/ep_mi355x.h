@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define EP_ABI_VERSION 7
+#define EP_ABI_VERSION 8
 
 /* Limits of the library. */
 #define EP_MAX_RANKS 1024
@@ -650,6 +650,19 @@ ep_status ep_debug_copy(void *dst, const void *src, int64_t nbytes, void *stream
 #define EP_KERNEL_TILES_256 4u /* tiles of 256 rows                   */
 ep_status ep_debug_matmul_kernels(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags,
                                   uint32_t *kernels);
+
+/* Test hook, as the one above: the kernels of ep_matmul and ep_matmul_fp8 for results of
+ * out_type (fp32: ep_matmul_fp8 alone).  Host only.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW. */
+ep_status ep_debug_product_kernels(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags,
+                                   int32_t out_type, uint32_t *kernels);
+
+/* Test hook, not part of the method: how ep_matmul_backward cuts its gradients for these
+ * sizes.  plan receives the rows of a tile (128 or 256) and the slices of the inner
+ * dimension (1: none) of the rows' gradient, then those of the weights'.  Host only.
+ * Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW. */
+ep_status ep_debug_backward_plan(int64_t num_rows, int32_t num_groups, int32_t inner, int32_t outer, uint32_t flags,
+                                 int32_t plan[4]);
 
 /* Profiling hook, not part of the method: the device-side timing slots of a
  * library built with EP_DEVICE_TIMING=1 ("Ascend DeepEP MoE Dispatch
