@@ -215,9 +215,10 @@ __device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int 
 // Few rows to a weight matrix: the weights are read once, and the waves of a
 // workgroup take a share of the inner dimension each, so that a narrow matrix
 // keeps many loads in flight.  A workgroup has 16 * MT rows by NT channel tiles
-// of 16; the KW waves join their sums, in a fixed order, through LDS.  For int8, bound by the memory where weights are many (32 groups
-// of 3 rows, 7168 x 4096 gated: 149 us, 6.3 TB/s of weights), else by the loads of
-// the CU with the most workgroups, ~24 bytes a clock (one row: 7.4 us).
+// of 16; the KW waves join their sums, in a fixed order, through LDS.  For int8, bound by the
+// memory where weights are many (32 groups of 3 rows, 7168 x 4096 gated: 154 us, 6.1 TB/s
+// of weights), else by the loads of the CU with the most workgroups, ~24 bytes a clock
+// (one row: 7.4 us).
 //
 // A wave has a ring of S stages of LDS to itself and no barrier before the end:
 // it loads 128 bytes of its rows and channels straight into a stage, eight
@@ -232,7 +233,7 @@ __device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int 
 // the channel tiles are the ups of the first half's columns.
 //
 // E4M3 rows and 16-bit rows take the same way: 32 groups of 3 E4M3 rows, 7168 x 4096 gated,
-// 148 us, 6.4 TB/s of weights; one row 6.8 us, a 16-bit one 10.5.
+// 162 us, 5.8 TB/s of weights, of 16-bit rows 303 us, 6.2; one row 6.8 us, a 16-bit one 10.5.
 //
 // Block scales: a step is a block, so its scales are loaded with it, one float a lane:
 // rows 0..16 * MT - 1, then the columns' block of the weights (gated: two).

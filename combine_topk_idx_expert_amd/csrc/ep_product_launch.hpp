@@ -55,7 +55,8 @@ ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
   return EP_OK;
 }
 
-// Which kernel (both sides measured on MI355X, with int8):
+// Which kernel (both sides measured on MI355X with int8; E4M3 and 16-bit products take the same
+// rules unmeasured, but for tall_tiles below):
 //  - tiles of 256 x 256 once they fill three quarters of the CUs; below that
 //    tiles of 128 x 256 while they fill three eighths (2048 x 7168 x 4096 gated: 67
 //    against 82 us; 8192 x 8192 x 8192: 256 x 256 by 10%);
@@ -64,7 +65,7 @@ ep_status launch_matmul_split(const MatmulArgs& a, hipStream_t s) {
 //    49; 1 x 7168 x 49152: 63 against 88 and 90, 64 rows of it 87 against 91 and 93).
 // Groups: their sizes are on the device.  A group of at most kFewRows rows is
 // the split's and a larger one the tiles'; each launch passes over the others'
-// groups.  No second launch where large groups cannot fill more than half of the tiles'
+// groups.  (The mean counts the groups' padding.)  No second launch where large groups cannot fill more than half of the tiles'
 // grid (8 groups of 72 rows, 7168 x 4096 gated: 72 us by the split alone, 84 by both),
 // or three eighths for tall groups, whose rows the split takes 64 at a time (8 of 1696,
 // 4672 x 318 gated: 46 us by tiles, 80 by the split); nor a first one where the mean

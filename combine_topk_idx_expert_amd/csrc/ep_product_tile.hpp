@@ -25,10 +25,13 @@ namespace ep {
 // Against steps of 64 bytes with four stages (ep_int8_tile.hpp) the loads ask for whole
 // lines of 128 bytes, half as many requests, and barriers are half as many.  Measured:
 // 16-bit, 65536 x 4096 x 4096 gated 1.64 to 1.69 ms (64-byte steps 1.85), 4096^3 102 us (115),
-// 8192^3 815 to 945 us with the clock; E4M3, 65536 x 4096 x 4096 gated 1.01 to 1.05 ms.
-// What bounds it (8192^3): 16-bit matrix instructions run 66% of the cycles, the rest goes to
-// barriers and to reads of LDS waited for; E4M3's 52%, and vector instructions, two thirds of
-// them the scaling, 38%, which leaves a tenth.  Under either the clock falls to 1.5 to 1.9 GHz.
+// 8192^3 815 to 945 us with the box and its clock; E4M3, 65536 x 4096 x 4096 gated 1.01 to 1.05 ms.
+// What bounds it (8192^3): 16-bit matrix instructions run 66% of the cycles (the library's 86%),
+// E4M3's 52%, beside vector instructions, two thirds of them the scaling, in 38%.  A SIMD's
+// two waves could run both at once, but pass the same barrier and so the same phase.  By count a
+// step of 256 x 256 reads 192 KiB of LDS and writes 64 KiB, at 128 bytes a clock 2048 cycles,
+// which is what its matrix instructions take (128 of 16 cycles a SIMD, E4M3 64 of 32); how
+// much of the rest is waiting for LDS was not measured.  The clock falls to 1.5 to 1.9 GHz.
 //
 // LDS image: 128 bytes a row, chunk ^ (row & 7).  Columns of a wave's channel tiles, rows
 // past the group's and channels past the last as in ep_int8_tile.hpp.  With block scales
