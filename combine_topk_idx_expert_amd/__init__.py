@@ -41,6 +41,7 @@ from ._native import (  # noqa: F401
     debug_e4m3_encode,
     debug_matmul_kernels,
     debug_product_kernels,
+    debug_split_shape,
     dispatch,
     dispatch_cached,
     expert_rows,

@@ -226,6 +226,8 @@ def lib() -> ctypes.CDLL:
         L.ep_debug_matmul_kernels.restype = i32
         L.ep_debug_product_kernels.argtypes = [i64, i32, i32, u32, i32, ctypes.POINTER(u32)]
         L.ep_debug_product_kernels.restype = i32
+        L.ep_debug_split_shape.argtypes = [i64, i32, i32, i32, u32, ctypes.POINTER(i32)]
+        L.ep_debug_split_shape.restype = i32
         L.ep_debug_backward_plan.argtypes = [i64, i32, i32, i32, u32, ctypes.POINTER(i32)]
         L.ep_debug_backward_plan.restype = i32
         L.ep_last_error.argtypes = []
@@ -1120,6 +1122,14 @@ def debug_product_kernels(num_rows: int, num_groups: int, outer: int, gated: boo
     code = 1 if dtype is None else _type(dtype, "dtype")
     _check(lib().ep_debug_product_kernels(num_rows, num_groups, outer, _GATED if gated else 0, code, ctypes.byref(bits)))
     return tuple(name for bit, name in _KERNELS.items() if bits.value & bit)
+
+
+def debug_split_shape(num_rows: int, num_groups: int, inner_bytes: int, outer: int, gated: bool = False) -> tuple:
+    """(rows, channels, waves) of a workgroup of any product's few-row kernel for these sizes, zeros where
+    it is not launched, by ep_debug_split_shape.  Host only."""
+    shape = (ctypes.c_int32 * 3)()
+    _check(lib().ep_debug_split_shape(num_rows, num_groups, inner_bytes, outer, _GATED if gated else 0, shape))
+    return tuple(shape)
 
 
 def debug_backward_plan(num_rows: int, num_groups: int, inner: int, outer: int, gated: bool = False) -> tuple:

@@ -44,3 +44,25 @@ extern "C" ep_status ep_debug_product_kernels(int64_t num_rows, int32_t num_grou
                                        : product_kernels<Bf16Math>(num_rows, num_groups, width, gated);
   return EP_OK;
 }
+
+extern "C" ep_status ep_debug_split_shape(int64_t num_rows, int32_t num_groups, int32_t inner_bytes, int32_t outer,
+                                          uint32_t flags, int32_t* shape) {
+  if (!shape) return fail(EP_ERR_NULL, "shape is NULL");
+  const ep_status st = validate_matmul(num_rows, num_groups, outer, flags);
+  if (st != EP_OK) return st;
+  if (inner_bytes < 1) return fail(EP_ERR_SHAPE, "inner_bytes %d must be positive", inner_bytes);
+  const bool gated = flags & EP_MATMUL_GATED;
+  MatmulArgs m{};
+  m.M = num_rows;
+  m.G = std::max(num_groups, 1);
+  m.N = outer;
+  m.K = inner_bytes;
+  m.width = gated ? outer / 2 : outer;
+  const uint32_t kernels = num_rows == 0 ? 0 : matmul_kernels(num_rows, num_groups, m.width, gated);
+  m.most = kernels == EP_KERNEL_SPLIT ? num_rows : kFewRows;
+  const SplitShape t = kernels & EP_KERNEL_SPLIT ? split_shape(m, gated) : SplitShape{};
+  shape[0] = t.rows * 16;
+  shape[1] = t.cols * 16;
+  shape[2] = t.waves;
+  return EP_OK;
+}

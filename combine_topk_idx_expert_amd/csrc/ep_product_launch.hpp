@@ -87,35 +87,45 @@ constexpr int64_t kFewRows = 64;
 // against 9.4 us; 32 groups of 3 rows: 154 against 160; from the L2, 8 groups of 79
 // rows, 3904 x 78: 9.3 against 7.1) and a CU has one workgroup or small ones (512
 // rows, two a CU: 27 against 23).
-template <typename AR, typename IO, bool GATED, int MT, int NT>
-ep_status launch_matmul_split(const MatmulArgs& a, int64_t blocks, hipStream_t s) {
+struct SplitShape {
+  int rows, cols, waves;  // sixteens of rows and channels
+};
+
+inline SplitShape split_shape(const MatmulArgs& a, bool gated) {
+  constexpr int kShapes[5][2] = {{1, 2}, {1, 4}, {2, 2}, {2, 4}, {4, 4}};
+  const int64_t mean = std::min(a.M / a.G + (a.M % a.G != 0), a.most);
+  int64_t least = INT64_MAX, blocks = 0;
+  SplitShape best{};
+  for (const auto& shape : kShapes) {
+    const int rows = 16 * shape[0], cols = (gated ? 8 : 16) * shape[1];
+    const int64_t n = (mean + rows - 1) / rows * a.G * ((a.width + cols - 1) / cols);
+    const int64_t cost = (n + kCUs - 1) / kCUs * (shape[0] + shape[1]);
+    if (cost > least) continue;  // (of equals the larger one)
+    least = cost;
+    blocks = n;
+    best = SplitShape{shape[0], shape[1], 2};
+  }
   const bool stream = a.K >= 2048 && (int64_t)a.G * a.N * a.K >= (int64_t)8 << 20;
-  return stream && (MT == 1 || blocks <= kCUs) ? launch_matmul_split<AR, IO, GATED, MT, NT, 4, 2>(a, s)
-                                               : launch_matmul_split<AR, IO, GATED, MT, NT, 2, 2>(a, s);
+  if (stream && (best.rows == 1 || blocks <= kCUs)) best.waves = 4;
+  return best;
+}
+
+template <typename AR, typename IO, bool GATED, int MT, int NT>
+ep_status launch_matmul_split(const MatmulArgs& a, int waves, hipStream_t s) {
+  return waves == 4 ? launch_matmul_split<AR, IO, GATED, MT, NT, 4, 2>(a, s)
+                    : launch_matmul_split<AR, IO, GATED, MT, NT, 2, 2>(a, s);
 }
 
 template <typename AR, typename IO, bool GATED>
 ep_status launch_matmul_few(const MatmulArgs& a, hipStream_t s) {
-  constexpr int kShapes[5][2] = {{1, 2}, {1, 4}, {2, 2}, {2, 4}, {4, 4}};
-  const int64_t mean = std::min(a.M / a.G + (a.M % a.G != 0), a.most);
-  int64_t least = INT64_MAX, blocks = 0;
-  int best = 0;
-  for (int i = 0; i < 5; ++i) {
-    const int rows = 16 * kShapes[i][0], cols = (GATED ? 8 : 16) * kShapes[i][1];
-    const int64_t n = (mean + rows - 1) / rows * a.G * ((a.width + cols - 1) / cols);
-    const int64_t cost = (n + kCUs - 1) / kCUs * (kShapes[i][0] + kShapes[i][1]);
-    if (cost > least) continue;  // (of equals the larger one)
-    least = cost;
-    blocks = n;
-    best = i;
-  }
-  switch (best) {
-    case 0: return launch_matmul_split<AR, IO, GATED, 1, 2>(a, blocks, s);
-    case 1: return launch_matmul_split<AR, IO, GATED, 1, 4>(a, blocks, s);
-    case 2: return launch_matmul_split<AR, IO, GATED, 2, 2>(a, blocks, s);
-    case 3: return launch_matmul_split<AR, IO, GATED, 2, 4>(a, blocks, s);
-    default: return launch_matmul_split<AR, IO, GATED, 4, 4>(a, blocks, s);
-  }
+  const SplitShape t = split_shape(a, GATED);
+  if (t.rows == 1)
+    return t.cols == 2 ? launch_matmul_split<AR, IO, GATED, 1, 2>(a, t.waves, s)
+                       : launch_matmul_split<AR, IO, GATED, 1, 4>(a, t.waves, s);
+  if (t.rows == 2)
+    return t.cols == 2 ? launch_matmul_split<AR, IO, GATED, 2, 2>(a, t.waves, s)
+                       : launch_matmul_split<AR, IO, GATED, 2, 4>(a, t.waves, s);
+  return launch_matmul_split<AR, IO, GATED, 4, 4>(a, t.waves, s);
 }
 
 // EP_KERNEL_* of the launches for M rows in G groups (0: dense) and `width` columns of out.

@@ -657,6 +657,12 @@ ep_status ep_debug_matmul_kernels(int64_t num_rows, int32_t num_groups, int32_t 
 ep_status ep_debug_product_kernels(int64_t num_rows, int32_t num_groups, int32_t outer, uint32_t flags,
                                    int32_t out_type, uint32_t *kernels);
 
+/* Test hook, as the ones above, for every product: the rows and channels of a workgroup of
+ * the few-row kernel (EP_KERNEL_SPLIT) and its waves, zeros where it is not launched.
+ * inner_bytes: of a row.  Host only.  Errors: EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_OVERFLOW. */
+ep_status ep_debug_split_shape(int64_t num_rows, int32_t num_groups, int32_t inner_bytes, int32_t outer,
+                               uint32_t flags, int32_t shape[3]);
+
 /* Test hook, not part of the method: how ep_matmul_backward cuts its gradients for these
  * sizes.  plan receives the rows of a tile (128 or 256) and the slices of the inner
  * dimension (1: none) of the rows' gradient, then those of the weights'.  Host only.
