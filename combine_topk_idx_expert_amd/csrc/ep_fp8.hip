@@ -50,7 +50,8 @@ extern "C" ep_status ep_debug_split_shape(int64_t num_rows, int32_t num_groups, 
   if (!shape) return fail(EP_ERR_NULL, "shape is NULL");
   const ep_status st = validate_matmul(num_rows, num_groups, outer, flags);
   if (st != EP_OK) return st;
-  if (inner_bytes < 1) return fail(EP_ERR_SHAPE, "inner_bytes %d must be positive", inner_bytes);
+  if (inner_bytes < 1 || inner_bytes > 2 * EP_MAX_MATMUL_INNER)
+    return fail(EP_ERR_SHAPE, "inner_bytes %d must lie in [1, %d]", inner_bytes, 2 * EP_MAX_MATMUL_INNER);
   const bool gated = flags & EP_MATMUL_GATED;
   MatmulArgs m{};
   m.M = num_rows;

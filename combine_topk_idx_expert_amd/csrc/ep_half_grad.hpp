@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256) void join_slices_kernel(MatmulArgs a, const fl
 // Rounded to the rows' type, as the products' operands have to be; their sums are fp32.  s
 // comes from the hardware's exp2 and reciprocal, as in silu: a step of fp32 each, and less
 // than 2^-17 of s from the rounded exponent, far below that rounding.  Scaled by 2^-16, the
-// denominator stays in fp32 down to gates of -98, where s falls below its smallest value.
+// denominator stays in fp32 down to gates of -98; an s below 2^-142 is 0.
 // The small factors are multiplied first, and by half, since s (1 + g (1 - s)) reaches 1.1: a
 // product leaves fp32 only if the gradient does.  g and u that were rounded to an infinity
 // count as fp32's largest, so that a shut gate, or a grad of 0, gives 0 and not NaN.

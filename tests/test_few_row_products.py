@@ -49,7 +49,9 @@ def test_shapes_are_named_for_sizes(L):
     assert ep.debug_split_shape(8192, 0, 8192, 8192) == ep.debug_split_shape(0, 0, 64, 64) == (0, 0, 0)
     shape = (ctypes.c_int32 * 3)()
     assert L.ep_debug_split_shape(1, 0, 64, 64, 0, None) == S.ERR_NULL
-    assert L.ep_debug_split_shape(1, 0, 0, 64, 0, shape) == S.ERR_SHAPE
+    for inner in (0, -1, 2 * 131056 + 1, (1 << 31) - 1):
+        assert L.ep_debug_split_shape(1, 0, inner, 64, 0, shape) == S.ERR_SHAPE
+    assert L.ep_debug_split_shape(1, 4096, 2 * 131056, 1 << 20, 0, shape) == S.OK
     assert L.ep_debug_split_shape(1, 0, 64, 63, 1, shape) == S.ERR_SHAPE
     assert L.ep_debug_split_shape(1 << 31, 0, 64, 64, 0, shape) == S.ERR_OVERFLOW
 
